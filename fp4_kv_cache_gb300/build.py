@@ -35,7 +35,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + [os.path.join(os.path.dirname(HERE), "include", "csa2.h"), __file__]
+        + glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:

@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import csa2
+from . import csa2, paged
 
 
 @dataclass
@@ -97,6 +97,62 @@ def reuse_layer(cache: Cache, x: LayerInput, idx: torch.Tensor, window: int = 12
     """Reuse mode: attention over the latest Top-K indices; no indexer work."""
     out, lse = _attend(cache, x, idx, window, d_v, sm_scale, d_status, stream)
     return LayerOutput(out, lse, idx)
+
+
+@dataclass
+class PagedState:
+    """A batch's pages, shared by the layers that hold the same rows; every step updates it."""
+    lens: torch.Tensor          # int32 [B] rows held
+    block_table: torch.Tensor   # int32 [B, W]
+    free_pages: torch.Tensor    # int32 [pages]
+    n_free: torch.Tensor        # int32 [1]
+
+
+@dataclass
+class PagedInput:
+    """One step's new tokens, requests one after another: queries, cache rows, and how many of each."""
+    q: torch.Tensor             # bf16 [T, H, d], not rotated
+    x: torch.Tensor             # bf16 [T, d] cache rows, not rotated
+    delta: torch.Tensor         # int32 [B] rows added (or, below 0, taken back)
+    cos_sin: Optional[torch.Tensor] = None      # f32 [n_pos, rope_dim]; None: no rotation
+    pos: Optional[torch.Tensor] = None          # int32 [axes, T]; None: each row's position in its request
+    sections: Optional[tuple] = None            # pairs of each axis
+
+
+@dataclass
+class PagedOutput:
+    out: torch.Tensor           # bf16 [T, H, d_v]
+    lse: Optional[torch.Tensor]
+    plan: "paged.PagePlan"
+
+
+def paged_layer(cache: "paged.PagedCache", state: PagedState, x: PagedInput, window: int = 0, d_v: int = 512,
+                sm_scale: Optional[float] = None, d_status=None, stream=None) -> PagedOutput:
+    """A layer over a paged cache, whole contexts or (the schedule's "swa" layers) the last `window`
+    rows: the step's bookkeeping, RoPE on the queries, the cache write with RoPE, then attention.
+    Rows of x past the step's last token are neither written nor attended."""
+    T = x.q.shape[0]
+    plan = paged.page_plan(state.lens, x.delta, state.block_table, state.free_pages, state.n_free, cache.page, T,
+                           in_place=True, d_status=d_status, stream=stream)
+    return _paged_attend(cache, state, x, plan, window, d_v, sm_scale, d_status, stream)
+
+
+def paged_layer_again(cache: "paged.PagedCache", state: PagedState, x: PagedInput, plan: "paged.PagePlan",
+                      window: int = 0, d_v: int = 512, sm_scale: Optional[float] = None, d_status=None,
+                      stream=None) -> PagedOutput:
+    """paged_layer for a further layer of the same step: its own cache and input, the step's plan."""
+    return _paged_attend(cache, state, x, plan, window, d_v, sm_scale, d_status, stream)
+
+
+def _paged_attend(cache, state, x, plan, window, d_v, sm_scale, d_status, stream) -> PagedOutput:
+    q, pos = x.q, x.pos
+    if x.cos_sin is not None:
+        pos = plan.row_pos if pos is None else pos
+        q = paged.rope_axes(q, pos, x.cos_sin, x.sections, None, d_status, stream)
+    paged.paged_write(cache, x.x, plan.slot, pos, x.cos_sin, x.sections, d_status, stream)
+    out, lse = paged.paged_attn(q, cache, state.block_table, state.lens, plan.cu, d_v=d_v, window=window,
+                                sm_scale=sm_scale, d_status=d_status, stream=stream)
+    return PagedOutput(out, lse, plan)
 
 
 # The report's schedule (§4.2.1; the review page's zero-based table): layers 0-1 SWA only;
