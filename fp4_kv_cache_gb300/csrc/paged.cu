@@ -416,6 +416,7 @@ bool paged_view(const csa2p_cache &c, PagedView &v)
     if (v.code_page < dense_c || v.code_page % 16 || v.scale_page < dense_s) return false;
     if (c.n_pages > 0 && (!c.codes || ((uintptr_t)c.codes & 15))) return false;
     if (c.n_pages > 0 && v.scale_row && !c.scales) return false;
+    if (c.fmt == CSA2P_NVFP4_E4M3_16 && (((uintptr_t)c.scales & 1) || v.scale_page % 2)) return false;
     v.codes = static_cast<const uint8_t *>(c.codes);
     v.scales = static_cast<const uint8_t *>(c.scales);
     v.n_pages = (int32_t)c.n_pages;

@@ -1,27 +1,33 @@
 // paged_attn.cu -- csa2p_attn on the tensor cores (sm_103a): attention of new tokens over a paged
 // latent cache shared by all heads (K = the row, V = its leading d_v dims).
 //
-// A request's queries are rows (token, head) = token x H + head, taken 128 at a time by a cluster
-// of two CTAs (cta_group::2, M = 128): each CTA owns 64 rows.  Per tile of 128 keys
-//   S [128 rows x 128 keys]  = Q K^T        (bf16 products, float32 sums, in tensor memory)
-//   O [128 rows x 512 dims] += P V          (P = 2^(S - m) in bf16)
-// Each CTA stages the 64 keys of its half: decoded once, they serve the whole pair as B operand
-// of S.  The B operand of O wants all 128 keys but only half of the dims in each CTA; its own
-// keys' rows are in place, the peer's keys' own-dims chunks are decoded over chunks that S no
-// longer needs.  So shared memory takes 104 KB of staging a tile instead of 2 x 147 KB, and the
-// MMA's operand reads halve too: staging and MMA both live off shared memory's 128 B a cycle.
+// A request's queries are rows (token, head) = token x H + head, taken 64 at a time by a CTA.  Per
+// tile of 128 keys, with the keys as the MMA's M dimension,
+//   S^T [128 keys x 64 rows]  = K Q^T         (bf16 products, float32 sums, in tensor memory)
+//   O^T [512 dims x 64 rows] += V^T P^T       (P = 2^(S - m) in bf16)
+// so that the decoded rows, staged once as nine chunks of 64 dims, are K's operand and, read the
+// other way, V's.  Chunk pairs go round: while the second product works through the dims in four
+// blocks, the staging warps refill the chunks that a block has left, and the first product of the
+// next tile follows them chunk by chunk.
+//
+// Softmax: a thread holds one key and half of the rows, so its logits are its own registers, its
+// weights are half of one 128-byte row of P^T, and the weights' sums stay apart per thread until
+// the row tile ends.  The maximum that the weights refer to is only moved when a logit exceeds it
+// by more than 16 (log2): then, and for a row tile's first keys, it is reduced over the threads
+// and O^T is rescaled.  Between moves a weight is at most 2^16: nothing is lost, since weights,
+// sums and products are floats.
 //
 // Decoding a 4-bit code: bits s e e m of a code placed as bf16's sign, two exponent and one
 // mantissa bit are the code's value x 2^-126 (subnormals included), so one bf16 product with
 // 2^126 x scale gives the exact value.  To save shifts the two values of a register are nibbles k
 // and k + 4 of a word: the eight channels of a 16-byte piece stand as 0 4 1 5 2 6 3 7, in Q the
-// same way, and the output's columns are put back in order when they are written.
+// same way, and the output is put back in order when it is written.
 //
-// Work is the list of (row tile, key tile) pairs, in equal runs for the clusters that fit the
-// GPU.  A row tile cut by the ends of runs leaves parts (O, m, l) in the workspace, which
-// a second kernel joins.  Every CTA works the list out for itself: no plan has to be made.
+// Work is the list of (row tile, key tile) pairs, in equal runs for the GPU's SMs.  A row tile
+// cut by the ends of runs leaves parts (O, m, l) in the workspace, which a second kernel joins.
+// Every CTA works the list out for itself: no plan has to be made.
 //
-// Keys past a row's bounds, in bad pages or of rows that are not finite are staged as zeros
+// Keys past a row tile's bounds, in bad pages or of rows that are not finite are staged as zeros
 // and marked, so that what they hold reaches no query that does not see them.
 #include "common.cuh"
 #include "internal.h"
@@ -30,29 +36,46 @@
 
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 512;           // warps 0-3 softmax, 4 MMA, 8-15 staging
-constexpr int kStageWarp = 8, kStageThreads = 256;
-constexpr int kRows = 128, kKeys = 128; // of a pair
-constexpr int kUnit = 8192;             // 64 rows x 64 dims of bf16, 128-byte swizzle
+constexpr int kThreads = 640;           // warps 0-7 softmax, 8 MMA, 9-19 staging
+constexpr int kMmaWarp = 8, kStageWarp = 9, kStageWarps = 11, kStageThreads = 32 * kStageWarps;
+constexpr int kTasks = 6;               // staging tasks of 32 channels a warp and tile, at most
+constexpr int kRing = 3;                // tiles whose rows are looked up: this one and two ahead
+constexpr int kRows = 64, kKeys = 128;
+constexpr int kQUnit = 8192;            // 64 rows x 64 dims of bf16, 128-byte swizzle
+constexpr int kChunk = 16384;           // 128 keys x 64 dims
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;           // O is rescaled when a maximum grows by more than 2^8
+constexpr float kLazy = 16.0f;          // the maximum moves when a logit is more than this above it
+constexpr float kUnset = 1e30f;         // -maximum of a row that has seen no key
 
-// shared memory: Q 9 units | K stage 0, 1: chunks 0..7 | chunk 8 | P 2 units | the rest
-constexpr int kOffK = 9 * kUnit, kOffR = kOffK + 16 * kUnit, kOffP = kOffR + kUnit, kOffMisc = kOffP + 2 * kUnit;
+// shared memory: Q 9 units | chunks 0..7 | chunk 8, or P^T once S has been computed | the rest
+constexpr int kOffK = 9 * kQUnit, kOffP = kOffK + 8 * kChunk, kOffMisc = kOffP + kChunk;
+
+struct RowAt { const uint8_t *code, *scale; };   // a key's row; code NULL: no key
+struct TileAt {                          // a key tile, for everyone
+    int64_t row0;                        // its row tile: first row in q, rows, place in lo and hi
+    int32_t rows, item;
+    int32_t key0;
+    uint32_t flags;                      // kFirst ..
+    int32_t nt;                          // key tiles of the row tile, over all CTAs
+};
+constexpr uint32_t kFirst = 1, kLast = 2;     // of this CTA's key tiles of the row tile
+constexpr uint32_t kEdge = 4;                 // some row does not see every key
+constexpr uint32_t kTail = 8, kPart = 16;     // the row tile began in a CTA before; others have parts of it
 
 struct Misc {
-    uint64_t full_k[2][3], full_z[2], full_p;   // the leader's: staged, probabilities written
-    uint64_t s_done[2], pv_done[2], info[2];    // each CTA's
-    uint64_t drained;
-    uint64_t valid[2][2], nan[2][2];            // [stage][half]: keys there, keys not finite
-    float top[2][2][64], sum[2][64];            // exchange between the halves of a row
-    int64_t scan[32];
-    int64_t start_unit, total, item_unit;       // this cluster's first unit; its item's first unit
+    uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
+    uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
+    RowAt row[kRing][kKeys];
+    TileAt tile[kRing];
+    float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
+    float red[4][kRows];
+    int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile
+    int64_t scan[kThreads / 32];
+    int64_t item_unit;                  // first unit of this CTA's first item
+    uint32_t nan[2][4];                 // keys with a value that is not finite
     int32_t b, j, off;
     uint32_t tmem;
     int32_t abort;
@@ -60,7 +83,7 @@ struct Misc {
 constexpr int kSmem = kOffMisc + (int)sizeof(Misc);
 static_assert(kSmem <= 232448, "does not fit the shared memory of a CTA");
 
-struct PartDesc {        // per cluster: the item it starts and does not finish
+struct PartDesc {        // per CTA: the row tile it starts and does not finish
     int32_t parts;       // 0: none
     int32_t rows;
     int64_t row0;
@@ -68,67 +91,24 @@ struct PartDesc {        // per cluster: the item it starts and does not finish
 
 struct AttnParams {
     PagedView C;
-    int32_t batch, n_tokens, H, d_v, width, window, ratio, chunks, v_chunks, n_pv;
+    int32_t batch, n_tokens, H, d_v, width, window, ratio, chunks, n_pv;
     float log2_scale;
+    uint32_t f0, f4;              // see decode
     const uint16_t *q;
     const int32_t *table, *lens, *cu, *pos0, *start;
     uint16_t *out;
     float *lse;
     uint32_t *d_status;
-    float *part_o, *part_ml;      // [2 clusters][128][d_v], [2 clusters][128][2]
-    PartDesc *desc;               // [clusters]
+    float *part_o, *part_ml;      // [2 CTAs][64][d_v], [2 CTAs][64][2]
+    PartDesc *desc;               // [CTAs]
 };
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_peer(uint32_t local, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void arrive_at(const uint64_t *bar, uint32_t rank)   // CTA `rank`'s barrier
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                 ::"r"(map_peer(tc::smem_u32(bar), rank)) : "memory");
-}
-__device__ __forceinline__ void st_peer_u8(const void *local, uint32_t rank, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(map_peer(tc::smem_u32(local), rank)), "r"(v) : "memory");
-}
-// Bounded wait that also sees what the peer CTA released.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int32_t *abort)
-{
-#pragma unroll 1
-    for (uint32_t i = 0; i < tc::kSpinLimit; ++i) {
-        uint32_t ok;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
-        if (ok) return true;
-        if ((i & 255u) == 255u && *(const volatile int32_t *)abort) return false;
-    }
-    return false;
-}
-__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void commit2(uint64_t *bar)         // arrives at both CTAs' barrier
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(tc::smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 __device__ __forceinline__ float ex2(float x)
 {
@@ -142,13 +122,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
 }
-// 128 softmax threads: barrier that tells all of them whether any has failed
-__device__ __forceinline__ bool softmax_sync(bool failed)
+using tc::mbar_wait;
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int32_t *abort)
+{
+    return mbar_wait(bar, parity, abort);
+}
+// 256 softmax threads: barrier that tells all of them whether one of them says yes
+__device__ __forceinline__ bool softmax_any(bool v)
 {
     uint32_t any;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.red.or.aligned.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any) : "r"((uint32_t)failed) : "memory");
+                 "barrier.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"((uint32_t)v) : "memory");
     return any != 0;
 }
 
@@ -156,9 +141,29 @@ __device__ __forceinline__ int sw128(int row, int piece)
 {
     return (row >> 3) * 1024 + (row & 7) * 128 + ((piece ^ (row & 7)) << 4);
 }
-__device__ __forceinline__ constexpr uint32_t instr(int n, int b_mn)   // M = 128, bf16 in, float32 sums
+// M = 128, N = 64, bf16 in, float32 sums; which operands lie with M or N contiguous
+__device__ __forceinline__ constexpr uint32_t instr(int a_mn, int b_mn)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(kRows >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
+}
+// Reduces 16 values per thread over a warp by halving; afterwards lane L holds value L / 2.
+template <bool MAX>
+__device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane)
+{
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+        const int o = 16 >> st, n = 16 >> st;
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = upper ? v[i] : v[i + n / 2], keep = upper ? v[i + n / 2] : v[i];
+            const float recv = __shfl_xor_sync(0xffffffffu, send, o);
+            v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
+        }
+    }
+    const float recv = __shfl_xor_sync(0xffffffffu, v[0], 1);
+    return MAX ? fmaxf(v[0], recv) : v[0] + recv;
 }
 
 // ------------------------------------------------------------------ decoding
@@ -173,125 +178,183 @@ __device__ __forceinline__ uint32_t mul2(uint32_t v, __nv_bfloat162 m)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// Sixteen channels of a row as they lie in the cache, and their scale byte.
-template <int FMT>
+// N x 8 channels of a row as they lie in the cache, and their scale bytes (NVFP4: two for 32
+// channels).  N = 4: a scale block of 32 channels; N = 2: half of one.
+template <int FMT, int N>
 struct Raw {
-    static constexpr int kWords = FMT == CSA2P_BF16 ? 8 : FMT == CSA2P_MXFP8 ? 4 : 2;
+    static constexpr int kWords = N * (FMT == CSA2P_BF16 ? 4 : FMT == CSA2P_MXFP8 ? 2 : 1);
     uint32_t w[kWords];
     uint32_t sb;
 };
 
+// Bytes of n channels' codes.
 template <int FMT>
-__device__ __forceinline__ void load_raw(Raw<FMT> &r, const uint8_t *codes, const uint8_t *scales, int part)
+__device__ __forceinline__ constexpr int code_bytes(int n)
 {
-    // part: which 16 channels of the row
-    if (FMT == CSA2P_BF16) {
-        const uint4 a = reinterpret_cast<const uint4 *>(codes)[2 * part], b = reinterpret_cast<const uint4 *>(codes)[2 * part + 1];
-        r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
-        r.w[4 % Raw<FMT>::kWords] = b.x; r.w[5 % Raw<FMT>::kWords] = b.y; r.w[6 % Raw<FMT>::kWords] = b.z; r.w[7 % Raw<FMT>::kWords] = b.w;
-        r.sb = 0;
-    } else if (FMT == CSA2P_MXFP8) {
-        const uint4 a = reinterpret_cast<const uint4 *>(codes)[part];
-        r.w[0] = a.x; r.w[1] = a.y; r.w[2 % Raw<FMT>::kWords] = a.z; r.w[3 % Raw<FMT>::kWords] = a.w;
-        r.sb = scales[part >> 1];
-    } else {
-        const uint2 a = reinterpret_cast<const uint2 *>(codes)[part];
-        r.w[0] = a.x; r.w[1] = a.y;
-        r.sb = FMT == CSA2P_NVFP4_E4M3_16 ? scales[part] : scales[part >> 1];
-    }
-}
-template <int FMT>
-__device__ __forceinline__ void zero_raw(Raw<FMT> &r)
-{
-#pragma unroll
-    for (int i = 0; i < Raw<FMT>::kWords; ++i) r.w[i] = 0u;
-    r.sb = FMT == CSA2P_NVFP4_E4M3_16 ? 0u : 127u;
+    return FMT == CSA2P_BF16 ? 2 * n : FMT == CSA2P_MXFP8 ? n : n / 2;
 }
 
-// Two 16-byte pieces (channels 0-7 and 8-15 in the order 0 4 1 5 2 6 3 7) of bf16.  Returns whether
-// a value or the scale is not finite; the pieces are then zero.  Scale bytes that would take a
-// product out of range (no quantised row has them) count as not finite.
-template <int FMT>
-__device__ __forceinline__ bool decode(const Raw<FMT> &r, uint4 (&o)[2])
+// The 8 N channels whose codes and scale begin there.
+template <int FMT, int N>
+__device__ __forceinline__ void load_raw(Raw<FMT, N> &r, const uint8_t *codes, const uint8_t *scale)
 {
-    uint32_t v[8];
-    bool bad = false;
+    constexpr int kW = Raw<FMT, N>::kWords;
+    if (kW == 2) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(codes);
+        r.w[0] = a.x;
+        r.w[1] = a.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kW / 4; ++i) {
+            const uint4 a = reinterpret_cast<const uint4 *>(codes)[i];
+            r.w[(4 * i) % kW] = a.x;
+            r.w[(4 * i + 1) % kW] = a.y;
+            r.w[(4 * i + 2) % kW] = a.z;
+            r.w[(4 * i + 3) % kW] = a.w;
+        }
+    }
+    if (FMT == CSA2P_BF16) r.sb = 0;
+    else if (FMT == CSA2P_NVFP4_E4M3_16 && N == 4) r.sb = *reinterpret_cast<const uint16_t *>(scale);
+    else r.sb = *scale;
+}
+template <int FMT, int N>
+__device__ __forceinline__ void zero_raw(Raw<FMT, N> &r)
+{
+#pragma unroll
+    for (int i = 0; i < Raw<FMT, N>::kWords; ++i) r.w[i] = 0u;
+    r.sb = FMT == CSA2P_NVFP4_E4M3_16 ? 0u : 127u;
+}
+// Whether these channels need decode_slow: scales that one product cannot apply, and what is not
+// finite.
+template <int FMT, int N>
+__device__ __forceinline__ bool unusual(const Raw<FMT, N> &r)
+{
+    constexpr int kW = Raw<FMT, N>::kWords;
+    uint32_t e = 0;
     if (FMT == CSA2P_BF16) {
-        uint32_t e = 0;
 #pragma unroll
-        for (int i = 0; i < Raw<FMT>::kWords; ++i) e |= ((r.w[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-        bad = e != 0;
+        for (int i = 0; i < kW; ++i) e |= (r.w[i] & 0x7f807f80u) + 0x00800080u;
+        return (e & 0x80008000u) != 0;
+    }
+    if (FMT == CSA2P_MXFP8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < kW; ++i) e |= (r.w[i] & 0x7f7f7f7fu) + 0x01010101u;
+        return (e & 0x80808080u) != 0 || r.sb > 134u;
+    }
+    if (FMT == CSA2P_NVFP4_E4M3_16) return (((r.sb & 0x7f7fu) + 0x0101u) & 0x8080u) != 0;
+    return r.sb > 128u;
+}
+
+// N 16-byte pieces (eight channels each, in the order 0 4 1 5 2 6 3 7) of bf16, nothing unusual
+// among them.
+//
+// 4-bit codes: n = two codes, one in the low bits of each half of a word; n x (2^12 + 2^6) has the
+// sign bit in its place and the other three in theirs, with nothing carried between, and one mask
+// keeps those.  With the codes 4 bits higher the factor is 2^8 + 2^2.  (The logic unit is what
+// bounds the staging; products go to the other one.  The factors come as parameters so that they
+// stay products.)
+template <int FMT, int N>
+__device__ __forceinline__ void decode(const Raw<FMT, N> &r, uint32_t (&v)[4 * N], uint32_t f0, uint32_t f4)
+{
+    constexpr int kW = Raw<FMT, N>::kWords;
+    if (FMT == CSA2P_BF16) {
+#pragma unroll
+        for (int h = 0; h < N; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                v[4 * h + 2 * k] = prmt(r.w[(4 * h + k) % Raw<FMT>::kWords], r.w[(4 * h + k + 2) % Raw<FMT>::kWords], 0x5410u);
-                v[4 * h + 2 * k + 1] = prmt(r.w[(4 * h + k) % Raw<FMT>::kWords], r.w[(4 * h + k + 2) % Raw<FMT>::kWords], 0x7632u);
+                v[4 * h + 2 * k] = prmt(r.w[(4 * h + k) % kW], r.w[(4 * h + k + 2) % kW], 0x5410u);
+                v[4 * h + 2 * k + 1] = prmt(r.w[(4 * h + k) % kW], r.w[(4 * h + k + 2) % kW], 0x7632u);
             }
     } else if (FMT == CSA2P_MXFP8) {
-        // code bits as bf16 bits: value x 2^-120; x 2^(120 + sb - 127), in two products for large scales
-        uint32_t e = 0;
+        // code bits as bf16 bits: value x 2^-120; x 2^(120 + sb - 127)
+        const __nv_bfloat162 m = bf2((r.sb + 120u) << 7);
 #pragma unroll
-        for (int i = 0; i < Raw<FMT>::kWords; ++i) e |= ((r.w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        bad = e != 0 || r.sb >= 247u;
-        const __nv_bfloat162 m = bf2((min(r.sb, 134u) + 120u) << 7);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < N; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t a = prmt(r.w[(2 * h) % Raw<FMT>::kWords], r.w[(2 * h + 1) % Raw<FMT>::kWords], 0x4400u + 0x1111u * k);
+                const uint32_t a = prmt(r.w[(2 * h) % kW], r.w[(2 * h + 1) % kW], 0x4400u + 0x1111u * k);
                 v[4 * h + k] = mul2((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), m);
             }
-        if (r.sb > 134u) {
-            const __nv_bfloat162 m2 = bf2((min(r.sb, 246u) - 134u + 127u) << 7);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], m2);
-        }
     } else {
-        const bool nv = FMT == CSA2P_NVFP4_E4M3_16;
+        constexpr bool nv = FMT == CSA2P_NVFP4_E4M3_16;
         // E8M0: x 2^(126 + sb - 127); E4M3: x 2^126, then the scale (both products exact)
-        const __nv_bfloat162 m = nv ? bf2(253u << 7) : bf2((min(r.sb, 128u) + 126u) << 7);
-        bad = nv ? (r.sb & 0x7fu) == 0x7fu : r.sb >= 253u;
+        const uint32_t mb = nv ? 253u * 0x00800080u : (r.sb + 126u) * 0x00800080u;
+        const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&mb);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t w = r.w[h];
-            v[4 * h] = mul2(((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u), m);
-            v[4 * h + 1] = mul2(((w << 8) & 0x80008000u) | ((w << 2) & 0x01c001c0u), m);
-            v[4 * h + 2] = mul2(((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u), m);
-            v[4 * h + 3] = mul2((w & 0x80008000u) | ((w >> 6) & 0x01c001c0u), m);
+        for (int h = 0; h < N; ++h) {
+            const uint32_t w = r.w[h % kW], z = w >> 8;
+            v[4 * h] = mul2(((w & 0x000f000fu) * f0) & 0x81c081c0u, m);
+            v[4 * h + 1] = mul2(((w & 0x00f000f0u) * f4) & 0x81c081c0u, m);
+            v[4 * h + 2] = mul2(((z & 0x000f000fu) * f0) & 0x81c081c0u, m);
+            v[4 * h + 3] = mul2(((z & 0x00f000f0u) * f4) & 0x81c081c0u, m);
         }
         if (nv) {
-            const uint32_t bits = ((r.sb & 0x80u) << 8) | ((r.sb & 0x7fu) << 4);       // the scale x 2^-120
-            const uint32_t sc = mul2(bits | (bits << 16), bf2(247u << 7));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], *reinterpret_cast<const __nv_bfloat162 *>(&sc));
-        } else if (r.sb > 128u) {
-            const __nv_bfloat162 m2 = bf2((min(r.sb, 252u) - 128u + 127u) << 7);
+            for (int h = 0; h < N; h += 2) {
+                const uint32_t sb = r.sb >> (4 * h), bits = ((sb & 0x80u) << 8) | ((sb & 0x7fu) << 4);   // the scale x 2^-120
+                const uint32_t sc = mul2(bits | (bits << 16), bf2(247u << 7));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], m2);
+                for (int i = 0; i < 8; ++i) v[4 * h + i] = mul2(v[4 * h + i], *reinterpret_cast<const __nv_bfloat162 *>(&sc));
+            }
         }
     }
-    if (bad) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0u;
+}
+
+// The same for anything, written over what decode left: each value is code x scale in float32
+// (exact), rounded to bf16 once.  If a value or a scale is not finite all are zero and the key's
+// bit is set in *nan.  Scale bytes that could take a value past float32 (no quantised row has
+// them) count as not finite.  Rare, and kept out of the loops' code.
+template <int FMT, int N>
+__device__ __noinline__ void decode_slow(Raw<FMT, N> r, uint8_t *u, int col0, int col_step, uint32_t *nan, uint32_t bit)
+{
+    uint32_t v[4 * N];
+    bool bad = false;
+#pragma unroll 1
+    for (int e = 0; e < 8 * N; ++e) {
+        float x;
+        uint32_t sb = r.sb;
+        if (FMT == CSA2P_BF16) {
+            x = __uint_as_float((r.w[e >> 1] >> (16 * (e & 1))) << 16);
+            bad |= !isfinite(x);
+        } else if (FMT == CSA2P_MXFP8) {
+            x = e4m3_value((r.w[e >> 2] >> (8 * (e & 3))) & 0xffu);
+            bad |= x != x || sb >= 247u;
+            x *= e8m0_value(min(sb, 254u));
+        } else {
+            const uint32_t c = (r.w[e >> 3] >> (4 * (e & 7))) & 15u;
+            x = c & 8u ? -e2m1_mag(c & 7u) : e2m1_mag(c & 7u);
+            if (FMT == CSA2P_NVFP4_E4M3_16) {
+                x *= e4m3_value((sb >> (8 * (e >> 4))) & 0xffu);
+                bad |= x != x;
+            } else {
+                bad |= sb >= 253u;
+                x *= e8m0_value(min(sb, 254u));
+            }
+        }
+        const int at = 2 * (e & 3) + ((e & 7) >> 2);          // place of channel e within its eight
+        const __nv_bfloat16 b = __float2bfloat16_rn(x);
+        const uint32_t h = (uint32_t)__bfloat16_as_ushort(b) << (16 * (at & 1));
+        uint32_t &d = v[4 * (e >> 3) + (at >> 1)];
+        d = (at & 1) ? d | h : h;
     }
-    o[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    o[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    return bad;
+    if (bad) atomicOr(nan, bit);
+#pragma unroll 1
+    for (int i = 0; i < N; ++i)                               // piece i at column col0 ^ (i x col_step)
+        *reinterpret_cast<uint4 *>(u + (col0 ^ (i * col_step))) =
+            bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // ------------------------------------------------------------------ the work list
 struct Item {                 // a row tile
     int32_t b, j;             // request, row tile of it
-    int32_t first, tokens;    // its tokens in q
-    int32_t rows;             // rows of the tile (1..128)
+    int32_t rows;             // rows of the tile (1..64)
     int32_t len;              // rows of the cache that the table can reach
-    int64_t p0;               // position of token 0
+    int64_t row0, p0;         // first row in q; position of the request's token 0
     int32_t lo, hi;           // keys that some row of the tile may see
+    int32_t lo_all, hi_all;   // keys that every row of the tile sees
     int32_t k0, nt;           // key tiles k0 .. k0 + nt - 1 (at least one, maybe of no key)
+    bool more;                // the request has further row tiles
     bool beyond;              // some visible row lies past the table
-
-    __device__ __forceinline__ int64_t row0(int H) const { return (int64_t)first * H + (int64_t)j * kRows; }
 };
 
 __device__ __forceinline__ void request_tokens(const AttnParams &P, int b, int32_t &first, int32_t &tokens)
@@ -316,35 +379,37 @@ __device__ __forceinline__ void bounds(const AttnParams &P, int64_t p, int32_t l
     if (P.window > 0 && e - P.window > l) l = e - P.window;
     lo = (int32_t)(l < hi ? l : hi);
 }
-__device__ __forceinline__ void load_item(const AttnParams &P, int b, int j, Item &it)
+__device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
 {
+    Item it;
     it.b = b;
     it.j = j;
-    request_tokens(P, b, it.first, it.tokens);
-    const int64_t total = (int64_t)it.tokens * P.H;
-    it.rows = (int32_t)(total - (int64_t)j * kRows < kRows ? total - (int64_t)j * kRows : kRows);
+    int32_t first, tokens;
+    request_tokens(P, b, first, tokens);
+    const int64_t left = (int64_t)tokens * P.H - (int64_t)j * kRows;
+    it.row0 = (int64_t)first * P.H + (int64_t)j * kRows;
+    it.rows = (int32_t)(left < kRows ? left : kRows);
+    it.more = left > kRows;
     const int32_t held = max(P.lens[b], 0);
     const int64_t reach = (int64_t)P.width << P.C.shift;
     it.len = (int32_t)(held < reach ? held : reach);
-    it.p0 = P.pos0 ? (int64_t)P.pos0[b] : (int64_t)held - it.tokens;
+    it.p0 = P.pos0 ? (int64_t)P.pos0[b] : (int64_t)held - tokens;
     const int32_t start = P.start ? P.start[b] : 0;
     const uint32_t r0 = (uint32_t)j * kRows;               // rows of a call are fewer than 2^31
     const uint32_t t0 = r0 / (uint32_t)P.H, t1 = (r0 + it.rows - 1) / (uint32_t)P.H;
-    int32_t lo0, hi0, lo1, hi1;
     int64_t e0, e1;
-    bounds(P, it.p0 + t0, it.len, start, lo0, hi0, e0);
-    bounds(P, it.p0 + t1, it.len, start, lo1, hi1, e1);
-    it.lo = lo0;
-    it.hi = hi1;
+    bounds(P, it.p0 + t0, it.len, start, it.lo, it.hi_all, e0);
+    bounds(P, it.p0 + t1, it.len, start, it.lo_all, it.hi, e1);
     it.beyond = held > it.len && e1 > it.len;
-    it.k0 = lo0 / kKeys;
-    it.nt = hi1 > lo0 ? (hi1 + kKeys - 1) / kKeys - it.k0 : 1;
+    it.k0 = it.lo / kKeys;
+    it.nt = it.hi > it.lo ? (it.hi + kKeys - 1) / kKeys - it.k0 : 1;
+    return it;
 }
 
-// Walks a cluster's run of (row tile, key tile) units.
+// Walks a CTA's run of (row tile, key tile) units.
 struct Walk {
     Item it;
-    int32_t off, n;           // this cluster's key tiles of the item: off .. off + n - 1
+    int32_t off, n;           // this CTA's key tiles of the item: off .. off + n - 1
     int64_t left;             // units of the run after them
     int32_t at;               // tile of the item
 
@@ -359,7 +424,7 @@ struct Walk {
     {
         left = units;
         if (units <= 0) return false;
-        load_item(P, M.b, M.j, it);
+        it = load_item(P, M.b, M.j);
         off = M.off;
         take();
         return true;
@@ -370,11 +435,11 @@ struct Walk {
         if (++at < n) return true;
         if (left <= 0) return false;
         int b = it.b, j = it.j + 1;
-        if ((int64_t)j * kRows >= (int64_t)it.tokens * P.H) {
+        if (!it.more) {
             j = 0;
             do ++b; while (b < P.batch - 1 && row_tiles(P, b) == 0);
         }
-        load_item(P, b, j, it);
+        it = load_item(P, b, j);
         off = 0;
         take();
         return true;
@@ -384,7 +449,7 @@ struct Walk {
     __device__ __forceinline__ int32_t key0() const { return (it.k0 + off + at) * kKeys; }
 };
 
-// Block-wide exclusive sum over the 512 threads.
+// Block-wide exclusive sum over the threads.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *buf, int64_t &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -408,32 +473,32 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *buf, int64_t &
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int FMT>
+// FULL: rows of 576 channels with 512 values, so that the chunk counts are constants.
+template <int FMT, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ AttnParams P)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
+    const int chunks = FULL ? 9 : P.chunks, n_pv = FULL ? 4 : P.n_pv;
+    const int n_blocks = FULL ? 18 : P.C.d / 32, pairs = FULL ? 4 : min((chunks + 1) / 2, 4);
+    const bool tail = FULL || chunks > 8;             // chunk 8 is there
     Misc &M = *reinterpret_cast<Misc *>(sm + kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_rank();
-    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const int cta = blockIdx.x, ctas = gridDim.x;
 
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            for (int g = 0; g < 3; ++g) tc::mbar_init(&M.full_k[s][g], 2 * kStageThreads / 32);
-            tc::mbar_init(&M.full_z[s], 2 * kStageThreads / 32);
-            tc::mbar_init(&M.info[s], 2 * kStageThreads / 32);
-            tc::mbar_init(&M.s_done[s], 1);
-            tc::mbar_init(&M.pv_done[s], 1);
-        }
+        for (int g = 0; g < 5; ++g) tc::mbar_init(&M.full_k[g], 16);
+        for (int j = 0; j < 4; ++j) tc::mbar_init(&M.pv_done[j], 1);
+        tc::mbar_init(&M.s_done, 1);
         tc::mbar_init(&M.full_p, 8);
         tc::mbar_init(&M.drained, 1);
+        for (int i = 0; i < kRing; ++i) tc::mbar_init(&M.rows[i], 4);
         tc::fence_mbar_init();
         M.abort = 0;
-        M.start_unit = -1;
     }
-    if (warp == 4) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&M.tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if (tid < 8) M.nan[tid >> 2][tid & 3] = 0;
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&M.tmem, 512);
+        tc::tmem_relinquish();
     }
     pdl_wait();
     pdl_allow_dependents();
@@ -467,427 +532,487 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         }
         own = 0;
         int b = rb;
-        Item it;
+#pragma unroll 1
         for (int64_t i = i0; i < i1; ++i) {
             while (tiles_before[b + 1] <= i) ++b;
-            load_item(P, b, (int)(i - tiles_before[b]), it);
-            own += it.nt;
+            own += load_item(P, b, (int)(i - tiles_before[b])).nt;
         }
         int64_t u = block_scan(own, M.scan, total);
-        share = (total + clusters - 1) / clusters;
-        const int64_t mine = share * cluster;
+        share = (total + ctas - 1) / ctas;
+        const int64_t mine = share * cta;
         if (mine < total && mine >= u && mine < u + own) {  // this thread's items hold the run's start
             b = rb;
+#pragma unroll 1
             for (int64_t i = i0; i < i1; ++i) {
                 while (tiles_before[b + 1] <= i) ++b;
-                load_item(P, b, (int)(i - tiles_before[b]), it);
-                if (mine < u + it.nt) {
+                const int j = (int)(i - tiles_before[b]), nt = load_item(P, b, j).nt;
+                if (mine < u + nt) {
                     M.b = b;
-                    M.j = it.j;
+                    M.j = j;
                     M.off = (int32_t)(mine - u);
                     M.item_unit = u;
                     break;
                 }
-                u += it.nt;
+                u += nt;
             }
         }
     }
-    const int64_t start = share * cluster;
+    const int64_t start = share * cta;
     const int64_t units = start < total ? (start + share < total ? share : total - start) : 0;
     tc::tc_fence_before();
     __syncthreads();
-    cluster_sync();                          // barriers and tensor memory of both CTAs are there
     tc::tc_fence_after();
-    const uint32_t tmem = M.tmem;            // O: columns 0..255 (two blocks), S: 256 + 64 (tile & 1)
-    if (tid == 0 && rank == 0) P.desc[cluster].parts = 0;
+    const uint32_t tmem = M.tmem;            // S^T: columns 0..63, O^T block j: 64 + 64 j ..
+    if (tid == 0) P.desc[cta].parts = 0;
 
     if (warp >= kStageWarp) {
         // ============================================================ staging
-        const int t = tid - kStageWarp * 32, key = t >> 2, quarter = t & 3;
-        Walk w;
-        bool go = w.begin(P, M, units), ok = true;
-        // slot of a key of the walk's tile (-1: none)
-        auto slot_of = [&](const Walk &v, int half) -> int32_t {
-            const int32_t k = v.key0() + 64 * half + key;
-            if (k < v.it.lo || k >= v.it.hi) return -1;
-            const int32_t id = P.table[(int64_t)v.it.b * P.width + (k >> P.C.shift)];
-            if (id < 0 || id >= P.C.n_pages) {
-                if (quarter == 0 && half == (int)rank) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
-                return -1;
-            }
-            return (int32_t)(((uint32_t)id << P.C.shift) + (k & ((1 << P.C.shift) - 1)));
-        };
-        constexpr int kBatch = FMT == CSA2P_BF16 ? 3 : FMT == CSA2P_MXFP8 ? 5 : 9;   // chunks held in registers
-        const int n_groups = (P.chunks + 2) / 3;
-        Raw<FMT> own[kBatch];
-        auto load_own = [&](int32_t sl, int c0) {
-            const uint8_t *codes = P.C.codes + P.C.code_at(sl < 0 ? 0 : sl), *scales = P.C.scales + P.C.scale_at(sl < 0 ? 0 : sl);
+        // Task (chunk pair, 8 keys): lane (key, q) decodes the q-th scale block of 32 channels of
+        // the pair; eight lanes of a store hold eight keys, hence eight different columns.  Warp w
+        // takes tasks w, w + 11, ..; chunk 8 makes 16 tasks of half the size, spread so that each
+        // warp has about the same.  A task's registers are loaded for the next tile as soon as they
+        // are decoded, so a whole tile's rows are on their way from memory.
+        const int w = warp - kStageWarp, k7 = lane & 7, q = lane >> 3;
+        const int j0 = w < 9 ? 6 + w : 3 * (w - 9), jn = w < 9 ? (w == 0 ? 2 : 1) : 3, jstep = w < 9 ? 9 : 1;
+        const int lane_code = q * code_bytes<FMT>(32), lane_scale = FMT == CSA2P_NVFP4_E4M3_16 ? 2 * q : q;
+        const int place = kOffK + (q >> 1) * kChunk + k7 * 128;
+        int col[4];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                zero_raw(own[i]);
-                if (sl >= 0 && c0 + i < P.chunks && (c0 + i) * 64 + quarter * 16 < P.C.d)
-                    load_raw(own[i], codes, scales, (c0 + i) * 4 + quarter);
-            }
+        for (int i = 0; i < 4; ++i) col[i] = ((4 * (q & 1) + i) ^ k7) << 4;
+        bool ok = true;
+        // how many of its tasks a warp has loaded ahead (registers)
+        constexpr int kAhead = FMT == CSA2P_BF16 ? 2 : FMT == CSA2P_MXFP8 ? 3 : kTasks;
+        auto live = [&](int task) { return task < 64 && (FULL || (task >> 4) < pairs); };
+        auto load_task = [&](Raw<FMT, 4> &r, int ring, int task) {
+            const RowAt a = M.row[ring][8 * (task & 15) + k7];
+            const int cp = task >> 4;
+            if (a.code != nullptr && (FULL || 4 * cp + q < n_blocks))
+                load_raw(r, a.code + lane_code + cp * code_bytes<FMT>(128), a.scale + lane_scale + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
+            else
+                zero_raw(r);
         };
-        int32_t sl_own = -1, sl_oth = -1;
-        if (go) {
-            sl_own = slot_of(w, (int)rank);
-            sl_oth = slot_of(w, 1 - (int)rank);
-            load_own(sl_own, 0);
+        Raw<FMT, 4> raw[kAhead];
+        if (units > 0) {
+            ok = wait_bar(&M.rows[0], 0, &M.abort);
+            if (ok)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (live(w + kStageWarps * k)) load_task(raw[k], 0, w + kStageWarps * k);
         }
-        for (uint32_t n = 0; go && ok; ++n) {
-            const uint32_t s = n & 1, ph = (n >> 1) & 1;
-            uint8_t *kbase = sm + kOffK + s * 8 * kUnit;
+        int ring = 0;                                 // n mod kRing, and the parity of the ring's round
+        uint32_t round = 0;
+#pragma unroll 1
+        for (uint32_t n = 0; n < (uint32_t)units; ++n) {
+            const bool more = n + 1 < (uint32_t)units;
+            const int ring1 = ring == kRing - 1 ? 0 : ring + 1;
+            const uint32_t round1 = ring1 == 0 ? round ^ 1 : round;
+            if (!__all_sync(0xffffffffu, ok)) break;
             // ---- the queries of a new row tile, once the old ones' last product is done
-            if (w.first()) {
-                if (n > 0) ok = wait_bar(&M.s_done[s ^ 1], ((n - 1) >> 1) & 1, &M.abort);
+            if (M.tile[ring].flags & kFirst) {
+                if (n > 0) ok = wait_bar(&M.s_done, (n - 1) & 1, &M.abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if (t == 0 && rank == 0 && w.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
-                const int pieces = P.C.d / 8, all = P.chunks * 8;
-                const int64_t r0 = w.it.row0(P.H) + 64 * rank;
-                const int mine = min(max(w.it.rows - 64 * (int)rank, 0), 64);
-#pragma unroll 6
-                for (int e = t; e < 64 * 72; e += kStageThreads) {
+                const int pieces = FULL ? 72 : P.C.d / 8, all = chunks * 8, rows = M.tile[ring].rows;
+                const uint16_t *src = P.q + M.tile[ring].row0 * P.C.d;
+#pragma unroll 4
+                for (int e = tid - 32 * kStageWarp; e < 64 * 72; e += kStageThreads) {
                     const int r = e / 72, p = e - 72 * r;
-                    if (p >= all) continue;
+                    if (!FULL && p >= all) continue;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < mine && p < pieces) v = *reinterpret_cast<const uint4 *>(P.q + (r0 + r) * P.C.d + 8 * p);
-                    *reinterpret_cast<uint4 *>(sm + (p >> 3) * kUnit + sw128(r, p & 7)) =
+                    if (r < rows && (FULL || p < pieces)) v = *reinterpret_cast<const uint4 *>(src + r * P.C.d + 8 * p);
+                    *reinterpret_cast<uint4 *>(sm + (p >> 3) * kQUnit + sw128(r, p & 7)) =
                         make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u), prmt(v.y, v.w, 0x7632u));
                 }
             }
-            // ---- the next tile's slots, looked up while this one is decoded
-            Walk nx = w;
-            const bool more = nx.next(P);
-            int32_t nx_own = -1, nx_oth = -1;
-            if (more) {
-                nx_own = slot_of(nx, (int)rank);
-                nx_oth = slot_of(nx, 1 - (int)rank);
-            }
-            // ---- own keys
-            if (n >= 2) ok = wait_bar(&M.pv_done[s], ((n - 2) >> 1) & 1, &M.abort);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            bool bad = false;
+            if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
+            int freed = n > 0 ? -1 : 4;               // last block of the tile before known to be done
 #pragma unroll
-            for (int c = 0; c < 9; ++c) {
-                if (c < P.chunks) {
-                    if (kBatch < 9 && c > 0 && c % kBatch == 0) load_own(sl_own, c);
-                    if (c == 8 && n > 0) ok = wait_bar(&M.s_done[s ^ 1], ((n - 1) >> 1) & 1, &M.abort) && ok;
-                    uint4 o[2];
-                    bad |= decode(own[c % kBatch], o);
-                    uint8_t *u = c < 8 ? kbase + c * kUnit : sm + kOffR;
-                    *reinterpret_cast<uint4 *>(u + sw128(key, 2 * quarter)) = o[0];
-                    *reinterpret_cast<uint4 *>(u + sw128(key, 2 * quarter + 1)) = o[1];
+            for (int k = 0; k < kTasks; ++k) {
+                const int task = w + kStageWarps * k;
+                if (!live(task)) continue;
+                const int kg = task & 15, cp = task >> 4;
+                Raw<FMT, 4> &r = raw[k % kAhead];
+                uint32_t v[16];
+                decode(r, v, P.f0, P.f4);
+                const int need = min(cp, n_pv - 1);
+                if (freed < need) {
+                    ok = wait_bar(&M.pv_done[need], (n - 1) & 1, &M.abort) && ok;
+                    freed = need;
                 }
-                if (c % 3 == 2 || c == P.chunks - 1) {
-                    if (c < P.chunks || c / 3 < n_groups) {
-                        if (c == min(3 * (c / 3) + 2, P.chunks - 1)) {
-                            tc::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) arrive_at(&M.full_k[s][c / 3], 0);
-                        }
-                    }
-                }
-            }
-            // which keys are there and finite: both CTAs' softmax wants it
-            {
-                const uint32_t have = __ballot_sync(0xffffffffu, sl_own >= 0), nan = __ballot_sync(0xffffffffu, bad);
-                if (lane < 2) {
-                    uint32_t hv = 0, nv = 0;
+                uint8_t *u = sm + place + cp * 2 * kChunk + kg * 1024;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        hv |= ((have >> (4 * k)) & 1u) << k;
-                        nv |= (((nan >> (4 * k)) & 15u) ? 1u : 0u) << k;
-                    }
-                    const uint8_t *pv = reinterpret_cast<const uint8_t *>(&M.valid[s][rank]) + (warp - kStageWarp);
-                    const uint8_t *pn = reinterpret_cast<const uint8_t *>(&M.nan[s][rank]) + (warp - kStageWarp);
-                    st_peer_u8(pv, (uint32_t)lane, hv);
-                    st_peer_u8(pn, (uint32_t)lane, nv);
-                    arrive_at(&M.info[s], (uint32_t)lane);
-                }
-            }
-            // ---- the peer's keys, this CTA's dims: over chunks that S has read
-            const bool own_dims = (int)rank * 2 < P.v_chunks;
-            Raw<FMT> oth[4];
-            {
-                const uint8_t *codes = P.C.codes + P.C.code_at(sl_oth < 0 ? 0 : sl_oth), *scales = P.C.scales + P.C.scale_at(sl_oth < 0 ? 0 : sl_oth);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (i >> 1) * 4 + 2 * (int)rank + (i & 1);
-                    zero_raw(oth[i]);
-                    if (sl_oth >= 0 && c < P.v_chunks && c * 64 + quarter * 16 < P.C.d) load_raw(oth[i], codes, scales, c * 4 + quarter);
-                }
-            }
-            if (more) load_own(nx_own, 0);
-            ok = wait_bar(&M.s_done[s], ph, &M.abort) && ok;
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (own_dims) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (i >> 1) * 4 + 2 * (int)rank + (i & 1);
-                    if (c < P.v_chunks) {
-                        uint4 o[2];
-                        decode(oth[i], o);
-                        uint8_t *u = kbase + (c ^ 2) * kUnit;
-                        *reinterpret_cast<uint4 *>(u + sw128(key, 2 * quarter)) = o[0];
-                        *reinterpret_cast<uint4 *>(u + sw128(key, 2 * quarter + 1)) = o[1];
-                    }
-                }
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                if (unusual(r)) decode_slow(r, u, col[0], 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + k7));
                 tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&M.full_k[cp]);
+                // the registers' next task: later in this tile, or in the next
+                if (k + kAhead < kTasks) {
+                    if (live(task + kStageWarps * kAhead)) load_task(r, ring, task + kStageWarps * kAhead);
+                } else if (more) {
+                    const int t1 = w + kStageWarps * ((k + kAhead) % kTasks);
+                    if (live(t1)) load_task(r, ring1, t1);
+                }
             }
-            __syncwarp();
-            if (lane == 0) arrive_at(&M.full_z[s], 0);
-            w = nx;
-            sl_own = nx_own;
-            sl_oth = nx_oth;
-            go = more;
+            if (tail) {
+                Raw<FMT, 2> r8[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (i >= jn) break;
+                    const RowAt a = M.row[ring][8 * (j0 + i * jstep) + k7];
+                    if (a.code != nullptr && (FULL || 16 + (q >> 1) < n_blocks))
+                        load_raw(r8[i], a.code + lane_code / 2 + code_bytes<FMT>(512), a.scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
+                    else
+                        zero_raw(r8[i]);
+                }
+                if (n > 0) ok = wait_bar(&M.pv_done[n_pv - 1], (n - 1) & 1, &M.abort) && ok;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (i >= jn) break;
+                    const int kg = j0 + i * jstep;
+                    uint32_t v[8];
+                    decode(r8[i], v, P.f0, P.f4);
+                    uint8_t *u = sm + kOffP + kg * 1024 + k7 * 128;
+                    const int c8 = ((2 * q) ^ k7) << 4;
+                    *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
+                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + k7));
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&M.full_k[4]);
+                }
+            }
+            ring = ring1;
+            round = round1;
         }
         if (!ok) M.abort = 1;
-    } else if (warp == 4) {
-        // ============================================================ MMA (the leader's one thread)
-        if (rank == 0 && lane == 0) {
+    } else if (warp == kMmaWarp) {
+        // ============================================================ MMA (one thread)
+        if (lane == 0) {
             const uint32_t base = tc::smem_u32(sm);
             const uint64_t dq = tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
-            const uint64_t dp = tc::smem_desc(base + kOffP, 16, 1024, tc::kSwizzle128B);
-            const uint64_t dr = tc::smem_desc(base + kOffR, 16, 1024, tc::kSwizzle128B);
-            Walk w;
-            bool go = w.begin(P, M, units), ok = true, pending = false, pending_first = false;
-            auto pv = [&](uint32_t n, bool first) {
-                const uint32_t s = n & 1;
-                ok = wait_bar(&M.full_p, n & 1, &M.abort) && wait_bar(&M.full_z[s], (n >> 1) & 1, &M.abort);
-                if (!ok) return;
-                tc::tc_fence_after();
-                const uint64_t dv = tc::smem_desc(base + kOffK + s * 8 * kUnit, kUnit, 1024, tc::kSwizzle128B);
+            const uint64_t dk = tc::smem_desc(base + kOffK, 16, 1024, tc::kSwizzle128B);
+            const uint64_t dv = tc::smem_desc(base + kOffK, kChunk, 1024, tc::kSwizzle128B);
+            const uint64_t dp = tc::smem_desc(base + kOffP, kChunk, 1024, tc::kSwizzle128B);
+            bool ok = true;
+            int ring = 0;
 #pragma unroll 1
-                for (int j = 0; j < P.n_pv; ++j)
+            for (uint32_t n = 0; n < (uint32_t)units; ++n) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma2(tmem + 128 * j, dp + (k >> 2) * (kUnit / 16) + (k & 3) * 2,
-                             dv + (4 * j + 2 * (k >> 2)) * (kUnit / 16) + (k & 3) * 128, instr(256, 1), !(first && k == 0));
-                commit2(&M.pv_done[s]);
-            };
-            uint32_t n = 0;
-            for (; go; ++n) {
-                const uint32_t s = n & 1;
-                if (w.first() && pending) {
-                    pv(n - 1, pending_first);
-                    pending = false;
-                    if (!ok) break;
-                }
-                const uint64_t dk = tc::smem_desc(base + kOffK + s * 8 * kUnit, 16, 1024, tc::kSwizzle128B);
-#pragma unroll 1
-                for (int g = 0; 3 * g < P.chunks; ++g) {
-                    ok = wait_bar(&M.full_k[s][g], (n >> 1) & 1, &M.abort);
+                for (int g = 0; g < 5; ++g) {
+                    if (2 * g >= chunks) break;
+                    ok = wait_bar(&M.full_k[g], n & 1, &M.abort);
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const int c = 3 * g + i;
-                        if (c < P.chunks) {
-                            const uint64_t b = c < 8 ? dk + c * (kUnit / 16) : dr;
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = 2 * g + i;
+                        if (c < 9 && c < chunks)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma2(tmem + 256 + 64 * s, dq + c * (kUnit / 16) + k * 2, b + k * 2, instr(128, 0), (c | k) != 0);
-                        }
+                                mma(tmem, dk + c * (kChunk / 16) + k * 2, dq + c * (kQUnit / 16) + k * 2, instr(0, 0), (c | k) != 0);
                     }
                 }
                 if (!ok) break;
-                commit2(&M.s_done[s]);
-                if (pending) {
-                    pv(n - 1, pending_first);
-                    if (!ok) break;
+                const bool first = (M.tile[ring].flags & kFirst) != 0;   // read before the softmax may go on
+                ring = ring == kRing - 1 ? 0 : ring + 1;
+                tc::tc_commit(&M.s_done);
+                ok = wait_bar(&M.full_p, n & 1, &M.abort);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= n_pv) break;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma(tmem + 64 + 64 * j, dv + j * (2 * kChunk / 16) + k * 128, dp + k * 128, instr(1, 1), !(first && k == 0));
+                    tc::tc_commit(&M.pv_done[j]);
                 }
-                pending = true;
-                pending_first = w.first();
-                go = w.next(P);
             }
-            if (ok && pending) pv(n - 1, pending_first);
             if (!ok) M.abort = 1;
-            commit2(&M.drained);                   // nothing may still run when the CTAs leave
+            tc::tc_commit(&M.drained);                // nothing may still run when the CTA leaves
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else {
         // ============================================================ softmax and output
-        const int row = tid & 63, half = tid >> 6;
-        const uint32_t lane_t = tmem + ((uint32_t)(warp * 32) << 16);
-        Walk w;
-        bool go = w.begin(P, M, units), failed = false;
-        int32_t lo = 0, hi = 0;
-        float m = -INFINITY, l = 0.0f;
-        int64_t unit = M.item_unit;                // first unit of the item
-        for (uint32_t n = 0; go; ++n) {
-            const uint32_t s = n & 1, ph = (n >> 1) & 1;
-            if (w.first()) {
-                const uint32_t f = (uint32_t)w.it.j * kRows + 64 * rank + row;
-                lo = hi = 0;
-                if (64 * (int)rank + row < w.it.rows) {
+        // Thread (key, half): the key of its tensor memory lane, rows 32 half .. 32 half + 31.
+        const int quad = warp & 3, half = warp >> 2, key_in = 32 * quad + lane, c_lo = 32 * half;
+        const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16) + c_lo;
+        Walk walk;                                    // of the upper half's threads: two tiles ahead
+        bool failed = false;
+        int ahead_ring = 0, ib = -1;
+        // What a tile needs, for everyone: where its keys' rows lie, and at a row tile's start the
+        // rows' bounds.
+        auto look = [&]() {
+            const int32_t key0 = walk.key0(), k = key0 + key_in;
+            RowAt a = {nullptr, nullptr};
+            if (k >= walk.it.lo && k < walk.it.hi) {
+                const int32_t id = P.table[(int64_t)walk.it.b * P.width + (k >> P.C.shift)];
+                if (id >= 0 && id < P.C.n_pages) {
+                    const int32_t sl = (int32_t)(((uint32_t)id << P.C.shift) + (k & ((1 << P.C.shift) - 1)));
+                    a.code = P.C.codes + P.C.code_at(sl);
+                    a.scale = P.C.scales + P.C.scale_at(sl);
+                } else {
+                    dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                }
+            }
+            M.row[ahead_ring][key_in] = a;
+            if (walk.first()) {
+                ++ib;
+                if (key_in < kRows) {                 // rows past the last: as the last
+                    int32_t lo, hi;
                     int64_t e;
-                    bounds(P, w.it.p0 + f / (uint32_t)P.H, w.it.len, P.start ? P.start[w.it.b] : 0, lo, hi, e);
+                    const uint32_t f = (uint32_t)walk.it.j * kRows + min(key_in, walk.it.rows - 1);
+                    bounds(P, walk.it.p0 + f / (uint32_t)P.H, walk.it.len, P.start ? P.start[walk.it.b] : 0, lo, hi, e);
+                    M.lo[ib & 3][key_in] = lo;
+                    M.hi[ib & 3][key_in] = hi;
                 }
-                m = -INFINITY;
-                l = 0.0f;
+                if (key_in == 0 && walk.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
             }
-            const int32_t k0 = w.key0() + 64 * half;
-            failed |= __any_sync(0xffffffffu, !wait_bar(&M.info[s], ph, &M.abort) || !wait_bar(&M.s_done[s], ph, &M.abort));
-            uint32_t r[64];
-            float top = -INFINITY;
-            if (!failed) {
-                tc::tc_fence_after();
-                tc::tc_ld_32x32b_x32(lane_t + 256 + 64 * s, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-                tc::tc_ld_32x32b_x32(lane_t + 256 + 64 * s + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-                tc::tc_wait_ld();
-                // keys of this half that the row sees, as bits
-                const int32_t a = max(lo - k0, 0), z = min(hi - k0, 64);
-                uint64_t see = z > a ? (~0ull >> (64 - (z - a))) << a : 0ull;
-                see &= M.valid[s][half];
-                const uint64_t nan = see & M.nan[s][half];
-                if (see != ~0ull) {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (!((see >> c) & 1ull)) r[c] = 0xff800000u;
-                }
-                if (nan) {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if ((nan >> c) & 1ull) r[c] = 0x7fc00000u;
-                }
-                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(r[c]));
-                top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * P.log2_scale;
+            if (key_in == 0) {
+                TileAt t;
+                t.row0 = walk.it.row0;
+                t.rows = walk.it.rows;
+                t.item = ib & 3;
+                t.key0 = key0;
+                t.nt = walk.it.nt;
+                t.flags = (walk.first() ? kFirst : 0) | (walk.last() ? kLast : 0) |
+                          (key0 < walk.it.lo_all || key0 + kKeys > walk.it.hi_all ? kEdge : 0) | (walk.off > 0 ? kTail : 0) |
+                          (walk.off > 0 || walk.off + walk.n < walk.it.nt ? kPart : 0);
+                M.tile[ahead_ring] = t;
             }
-            M.top[s][half][row] = top;
-            if (softmax_sync(failed)) { failed = true; break; }
-            top = fmaxf(top, M.top[s][half ^ 1][row]);
-            float f = 1.0f;
-            if (top > m + kLazy || (m == -INFINITY && top > -INFINITY)) {
-                f = ex2(m - top);                  // 0 for the first maximum
-                m = top;
-                l *= f;
-            }
-            const float mm = m == -INFINITY ? 0.0f : m;
-            float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t p[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const float x = ex2(fmaf(__uint_as_float(r[c]), P.log2_scale, -mm));
-                const float y = ex2(fmaf(__uint_as_float(r[c + 1]), P.log2_scale, -mm));
-                s4[c & 2] += x;
-                s4[(c & 2) + 1] += y;
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-                p[c / 2] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            // the previous product of this row tile has read P and written O
-            if (!w.first()) {
-                failed |= __any_sync(0xffffffffu, !wait_bar(&M.pv_done[s ^ 1], ((n - 1) >> 1) & 1, &M.abort));
-                if (!failed && __any_sync(0xffffffffu, f != 1.0f)) {
-                    tc::tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 128 * P.n_pv; c += 16) {
-                        uint32_t o[16];
-                        tc::tc_ld_32x32b_x16(lane_t + c, o);
-                        tc::tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tc::tc_st_32x32b_x16(lane_t + c, o);
-                    }
-                    tc::tc_wait_st();
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4 *>(sm + kOffP + half * kUnit + sw128(row, i)) =
-                    make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-            tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(&M.full_p, 0);
-            if (w.last()) {
-                // ---- output, or a part of it
-                failed |= __any_sync(0xffffffffu, !wait_bar(&M.pv_done[s], ph, &M.abort));
-                M.sum[half][row] = l;
-                if (softmax_sync(failed)) { failed = true; break; }
-                tc::tc_fence_after();
-                l += M.sum[half ^ 1][row];
-                const bool part = w.off > 0 || w.off + w.n < w.it.nt;
-                const int in_tile = 64 * (int)rank + row;
-                const bool live = in_tile < w.it.rows;
-                const int64_t grow = w.it.row0(P.H) + in_tile;
-                const int slot = 2 * cluster + (w.off > 0 ? 0 : 1);
-                if (part) {
-                    if (half == 0) {
-                        P.part_ml[((int64_t)slot * kRows + in_tile) * 2] = m;
-                        P.part_ml[((int64_t)slot * kRows + in_tile) * 2 + 1] = l;
-                    }
-                    if (w.off == 0 && tid == 0 && rank == 0) {
-                        PartDesc d;
-                        d.parts = (int32_t)((unit + w.it.nt - 1) / share - cluster + 1);
-                        d.rows = w.it.rows;
-                        d.row0 = w.it.row0(P.H);
-                        P.desc[cluster] = d;
-                    }
-                } else if (half == 0 && live && P.lse) {
-                    P.lse[grow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (lane == 0) tc::mbar_arrive(&M.rows[ahead_ring]);
+            ahead_ring = ahead_ring == kRing - 1 ? 0 : ahead_ring + 1;
+        };
+        bool more = false;                            // the walk has a tile that is not looked up yet
+        if (half == 1) {
+            more = walk.begin(P, M, units);
+            if (more) {
+                look();
+                more = walk.next(P);
+            }
+            if (more) {
+                look();
+                more = walk.next(P);
+            }
+        }
+        float l[32];                                  // sums of weights: this thread's key in each tile
+        int64_t unit = M.item_unit;                   // first unit of the item
+        int ring = 0;
+        uint32_t round = 0;
+#pragma unroll 1
+        for (uint32_t n = 0; n < (uint32_t)units; ++n) {
+            const uint32_t ph = n & 1;
+            failed |= __any_sync(0xffffffffu, !wait_bar(&M.rows[ring], round, &M.abort));
+            const TileAt &T = M.tile[ring];
+            const uint32_t flags = T.flags;
+            const bool first = flags & kFirst, have = M.row[ring][key_in].code != nullptr;
+            if (first) {
+                if (half == 0 && key_in < kRows) {
+                    M.m[key_in] = -INFINITY;
+                    M.nm[key_in] = kUnset;
                 }
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) l[c] = 0.0f;
+            }
+            if (half == 1 && more) {
+                // a tile looked up two ahead takes the place of the one before this one, whose staging
+                // and softmax are done
+                look();
+                more = walk.next(P);
+            }
+            failed |= __any_sync(0xffffffffu, !wait_bar(&M.full_k[tail ? 4 : pairs - 1], ph, &M.abort) || !wait_bar(&M.s_done, ph, &M.abort));
+            tc::tc_fence_after();
+            const bool nan = (M.nan[ph][quad] >> lane) & 1u;
+            // ---- logits that a row does not see become -inf, those of a key that is not finite NaN
+            if ((flags & kEdge) || __any_sync(0xffffffffu, nan || !have)) {
+                const int32_t key = T.key0 + key_in, item = T.item;
 #pragma unroll 1
-                for (int j = 0; j < P.n_pv; ++j)
+                for (int c0 = 0; c0 < 32; c0 += 16) {
+                    uint32_t r[16];
+                    tc::tc_ld_32x32b_x16(lane_t + c0, r);
+                    tc::tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const bool see = have && key >= M.lo[item][c_lo + c0 + c] && key < M.hi[item][c_lo + c0 + c];
+                        r[c] = !see ? 0xff800000u : nan ? 0x7fc00000u : r[c];
+                    }
+                    tc::tc_st_32x32b_x16(lane_t + c0, r);
+                }
+                tc::tc_wait_st();
+            }
+            bool moved = first;
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 16) {
-                        const int d0 = 256 * j + 128 * half + c;
-                        uint32_t o[16];
-                        tc::tc_ld_32x32b_x16(lane_t + 128 * j + c, o);
+            while (true) {
+                if (moved) {
+                    // ---- new maxima, reduced over the keys
+                    if (softmax_any(failed)) { failed = true; break; }
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 32; c0 += 16) {
+                        uint32_t r[16];
+                        float v[16];
+                        tc::tc_ld_32x32b_x16(lane_t + c0, r);
                         tc::tc_wait_ld();
 #pragma unroll
-                        for (int g = 0; g < 16; g += 8) {
-                            if (!live || d0 + g >= P.d_v) continue;
-                            float v[8];
+                        for (int c = 0; c < 16; ++c) {
+                            const float x = __uint_as_float(r[c]);
+                            v[c] = x != x ? -INFINITY : x * P.log2_scale;
+                        }
+                        const float top = warp_reduce16<true>(v, lane);
+                        if ((lane & 1) == 0) M.red[quad][c_lo + c0 + (lane >> 1)] = top;
+                    }
+                    softmax_any(false);
+                    if (tid < kRows) {
+                        const float top = fmaxf(fmaxf(M.red[0][tid], M.red[1][tid]), fmaxf(M.red[2][tid], M.red[3][tid])), m = M.m[tid];
+                        float f = 1.0f;
+                        if (top > m + kLazy || (m == -INFINITY && top > -INFINITY)) {
+                            f = ex2(m - top);         // 0 for the first maximum
+                            M.m[tid] = top;
+                            M.nm[tid] = -top;
+                        }
+                        M.fac[tid] = f;
+                    }
+                    softmax_any(false);
+                    if (!first) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                v[k] = __uint_as_float(o[g + 2 * k]);
-                                v[k + 4] = __uint_as_float(o[g + 2 * k + 1]);
+                        for (int c = 0; c < 32; ++c) l[c] *= M.fac[c_lo + c];
+                        failed |= __any_sync(0xffffffffu, !wait_bar(&M.pv_done[n_pv - 1], ph ^ 1, &M.abort));
+                        tc::tc_fence_after();
+#pragma unroll 1
+                        for (int j = 0; j < n_pv && !failed; ++j)
+#pragma unroll 1
+                            for (int c0 = 0; c0 < 32; c0 += 16) {
+                                uint32_t o[16];
+                                tc::tc_ld_32x32b_x16(lane_t + 64 + 64 * j + c0, o);
+                                tc::tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * M.fac[c_lo + c0 + i]);
+                                tc::tc_st_32x32b_x16(lane_t + 64 + 64 * j + c0, o);
                             }
-                            if (part) {
-                                float4 *dst = reinterpret_cast<float4 *>(P.part_o + ((int64_t)slot * kRows + in_tile) * P.d_v + d0 + g);
-                                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-                            } else {
-                                uint32_t x[4];
+                        tc::tc_wait_st();
+                    }
+                }
+                // ---- weights: their bf16 values go to P^T; their sums stay in the thread
+                uint32_t r[32], p[16];
+                tc::tc_ld_32x32b_x32(lane_t, r);
+                tc::tc_wait_ld();
+                float over = -INFINITY;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
-                                    x[k] = *reinterpret_cast<const uint32_t *>(&b);
-                                }
-                                *reinterpret_cast<uint4 *>(P.out + grow * P.d_v + d0 + g) = make_uint4(x[0], x[1], x[2], x[3]);
+                for (int c = 0; c < 32; c += 2) {
+                    const float x = fmaf(__uint_as_float(r[c]), P.log2_scale, M.nm[c_lo + c]);
+                    const float y = fmaf(__uint_as_float(r[c + 1]), P.log2_scale, M.nm[c_lo + c + 1]);
+                    over = fmaxf(over, fmaxf(x, y));
+                    const float ex = ex2(x), ey = ex2(y);
+                    r[c] = __float_as_uint(ex);
+                    r[c + 1] = __float_as_uint(ey);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(ex, ey);
+                    p[c / 2] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(sm + kOffP + sw128(key_in, 4 * half + i)) = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+                tc::fence_proxy_async_smem();
+                // a logit far above its row's maximum: once more, with the maximum moved
+                if (softmax_any(failed || (!moved && over > kLazy))) {
+                    if (moved) { failed = true; break; }
+                    moved = true;
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) l[c] += __uint_as_float(r[c]);
+                break;
+            }
+            if (failed) break;
+            tc::tc_fence_before();
+            if (tid < 4) M.nan[ph][tid] = 0;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&M.full_p);
+            if (flags & kLast) {
+                // ---- output, or a part of it: sums over the keys, then a lane has one dim of every row
+                const int rows = T.rows;
+                const int64_t row0 = T.row0;
+                const bool part = flags & kPart;
+                const int32_t nt = T.nt;
+#pragma unroll
+                for (int c0 = 0; c0 < 32; c0 += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = l[c0 + c];
+                    const float sum = warp_reduce16<false>(v, lane);
+                    if ((lane & 1) == 0) M.red[quad][c_lo + c0 + (lane >> 1)] = sum;
+                }
+                failed |= __any_sync(0xffffffffu, !wait_bar(&M.pv_done[n_pv - 1], ph, &M.abort));
+                if (softmax_any(failed)) { failed = true; break; }
+                tc::tc_fence_after();
+                const int64_t slot = (2 * (int64_t)cta + ((flags & kTail) ? 0 : 1)) * kRows;
+                if (tid < kRows) {
+                    const float s = (M.red[0][tid] + M.red[1][tid]) + (M.red[2][tid] + M.red[3][tid]), m = M.m[tid];
+                    M.fac[tid] = s == 0.0f ? 0.0f : 1.0f / s;
+                    if (part) {
+                        P.part_ml[(slot + tid) * 2] = m;
+                        P.part_ml[(slot + tid) * 2 + 1] = s;
+                    } else if (tid < rows && P.lse) {
+                        P.lse[row0 + tid] = s == 0.0f ? -INFINITY : (m + log2f(s)) * kLn2;
+                    }
+                    if (part && !(flags & kTail) && tid == 0) {
+                        PartDesc d;
+                        d.parts = (int32_t)((unit + nt - 1) / share - cta + 1);
+                        d.rows = rows;
+                        d.row0 = row0;
+                        P.desc[cta] = d;
+                    }
+                }
+                softmax_any(false);
+                // the dim that this lane's place stands for, and of the pair that it writes
+                const int dim_in = (key_in & ~7) | ((key_in & 1) << 2) | ((key_in & 7) >> 1);
+                const bool odd = (lane & 2) != 0;
+#pragma unroll 1
+                for (int j = 0; j < n_pv; ++j)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 32; c0 += 16) {
+                        const int r0 = c_lo + c0, dim = 128 * j + dim_in;
+                        if (r0 >= rows) break;
+                        uint32_t o[16];
+                        tc::tc_ld_32x32b_x16(lane_t + 64 + 64 * j + c0, o);
+                        tc::tc_wait_ld();
+                        if (part) {
+                            if (dim < P.d_v)
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) P.part_o[(slot + r0 + c) * P.d_v + dim] = __uint_as_float(o[c]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; c += 2) {     // lanes two apart hold neighbouring dims
+                                const float x = __uint_as_float(o[c]) * M.fac[r0 + c], y = __uint_as_float(o[c + 1]) * M.fac[r0 + c + 1];
+                                const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 2);
+                                const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(other, y) : __floats2bfloat162_rn(x, other);
+                                const int r = r0 + c + (odd ? 1 : 0);
+                                if (r < rows && dim < P.d_v)
+                                    *reinterpret_cast<__nv_bfloat162 *>(P.out + (row0 + r) * P.d_v + (dim & ~1)) = b;
                             }
                         }
                     }
                 tc::tc_fence_before();
+                unit += nt;
             }
-            const int32_t nt = w.it.nt, was = w.last();
-            go = w.next(P);
-            if (was) unit += nt;
+            ring = ring == kRing - 1 ? 0 : ring + 1;
+            round ^= ring == 0;
         }
         if (failed) M.abort = 1;
     }
     __syncthreads();
-    if (tid == 0) {
-        tc::mbar_wait_bounded(&M.drained, 0);
-        if (M.abort) dev_flag(P.d_status, CSA2_DEV_TIMEOUT);
-    }
+    if (tid == 0 && (!tc::mbar_wait_bounded(&M.drained, 0) || M.abort)) dev_flag(P.d_status, CSA2_DEV_TIMEOUT);
     tc::tc_fence_before();
     __syncthreads();
-    cluster_sync();
-    if (warp == 4) {
+    if (warp == kMmaWarp) {
         tc::tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
 // Joins the parts of cut row tiles: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A warp takes
-// a row; blockIdx.x = the cluster that began the row tile, whose part is its second slot and whose
-// further parts are the first slots of the clusters after it.
+// a row; blockIdx.x = the CTA that began the row tile, whose part is its second slot and whose
+// further parts are the first slots of the CTAs after it.
 __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_constant__ AttnParams P)
 {
     pdl_wait();
@@ -931,26 +1056,31 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
     }
 }
 
-// Clusters of two CTAs of this kernel that are resident at once on the current device.
-int attn_clusters()
-{
-    return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
-}
-
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+template <bool FULL>
+auto attn_kernel(int fmt) -> void (*)(AttnParams)
+{
+    switch (fmt) {
+    case CSA2P_MXFP4: return paged_attn_kernel<CSA2P_MXFP4, FULL>;
+    case CSA2P_NVFP4_E4M3_16: return paged_attn_kernel<CSA2P_NVFP4_E4M3_16, FULL>;
+    case CSA2P_MXFP8: return paged_attn_kernel<CSA2P_MXFP8, FULL>;
+    default: return paged_attn_kernel<CSA2P_BF16, FULL>;
+    }
+}
 
 } // namespace
 
 size_t paged_attn_ws_bytes(const csa2p_attn_args &a)
 {
-    const size_t slots = 2 * (size_t)attn_clusters() * kRows;
-    return up256(slots * a.d_v * sizeof(float)) + up256(slots * 2 * sizeof(float)) + up256(attn_clusters() * sizeof(PartDesc));
+    const size_t ctas = device_sm_count(), rows = 2 * ctas * kRows;
+    return up256(rows * a.d_v * sizeof(float)) + up256(rows * 2 * sizeof(float)) + up256(ctas * sizeof(PartDesc));
 }
 
 cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint16_t *out, float *lse, void *ws,
                               uint32_t *d_status, cudaStream_t s)
 {
-    const int clusters = attn_clusters();
+    const int ctas = device_sm_count();
     AttnParams P;
     P.C = v;
     P.batch = a.batch;
@@ -961,9 +1091,10 @@ cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint
     P.window = a.window;
     P.ratio = a.ratio_m;
     P.chunks = (v.d + 63) / 64;
-    P.v_chunks = (a.d_v + 63) / 64;
-    P.n_pv = (a.d_v + 255) / 256;
+    P.n_pv = (a.d_v + 127) / 128;
     P.log2_scale = a.sm_scale * 1.4426950408889634f;
+    P.f0 = (1u << 12) + (1u << 6);
+    P.f4 = (1u << 8) + (1u << 2);
     P.q = a.q;
     P.table = a.block_table;
     P.lens = a.lens;
@@ -973,21 +1104,19 @@ cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint
     P.out = out;
     P.lse = lse;
     P.d_status = d_status;
-    const size_t slots = 2 * (size_t)clusters * kRows;
+    const size_t rows = 2 * (size_t)ctas * kRows;
     char *w = static_cast<char *>(ws);
     P.part_o = reinterpret_cast<float *>(w);
-    w += up256(slots * a.d_v * sizeof(float));
+    w += up256(rows * a.d_v * sizeof(float));
     P.part_ml = reinterpret_cast<float *>(w);
-    w += up256(slots * 2 * sizeof(float));
+    w += up256(rows * 2 * sizeof(float));
     P.desc = reinterpret_cast<PartDesc *>(w);
-    auto k = v.fmt == CSA2P_MXFP4 ? paged_attn_kernel<CSA2P_MXFP4>
-             : v.fmt == CSA2P_NVFP4_E4M3_16 ? paged_attn_kernel<CSA2P_NVFP4_E4M3_16>
-             : v.fmt == CSA2P_MXFP8 ? paged_attn_kernel<CSA2P_MXFP8> : paged_attn_kernel<CSA2P_BF16>;
+    void (*k)(AttnParams) = v.d == 576 && a.d_v == 512 ? attn_kernel<true>(v.fmt) : attn_kernel<false>(v.fmt);
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k, dim3((unsigned)(2 * clusters)), dim3(kThreads), (size_t)kSmem, s, 2, P);
+    e = launch_pdl(k, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, s, 1, P);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_join_kernel, dim3((unsigned)clusters, kRows / 8), dim3(256), 0, s, 1, P);
+    return launch_pdl(paged_attn_join_kernel, dim3((unsigned)ctas, kRows / 8), dim3(256), 0, s, 1, P);
 }
 
 } // namespace csa2

@@ -55,9 +55,9 @@ typedef struct {
     int32_t page;           /* rows a page: a power of two, 1..65536                              */
     int64_t n_pages;        /* pages; n_pages * page < 2^31                                       */
     void *codes;            /* 16-byte aligned                                                    */
-    void *scales;           /* NULL for BF16                                                      */
+    void *scales;           /* NULL for BF16; NVFP4: 2-byte aligned                               */
     int64_t code_stride;    /* bytes between pages (0: dense); a multiple of 16                   */
-    int64_t scale_stride;   /* bytes between pages (0: dense); even                               */
+    int64_t scale_stride;   /* bytes between pages (0: dense); NVFP4: even                        */
 } csa2p_cache;
 
 /* ---------------------------------------------------------------------------------- */
