@@ -36,6 +36,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 namespace csa2 {
 namespace {
 
@@ -1058,6 +1060,27 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Shared memory beyond the default has to be asked for once per kernel and device.
+cudaError_t allow_smem(const void *kernel, int bytes)
+{
+    constexpr int kMaxDevices = 64, kKernels = 8;
+    static std::atomic<const void *> done[kMaxDevices][kKernels];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (known)
+        for (int i = 0; i < kKernels; ++i)
+            if (done[dev][i].load(std::memory_order_acquire) == kernel) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess || !known) return e;
+    for (int i = 0; i < kKernels; ++i) {
+        const void *none = nullptr;
+        if (done[dev][i].compare_exchange_strong(none, kernel, std::memory_order_acq_rel) || none == kernel) break;
+    }
+    return cudaSuccess;
+}
+
 template <bool FULL>
 auto attn_kernel(int fmt) -> void (*)(AttnParams)
 {
@@ -1112,7 +1135,7 @@ cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint
     w += up256(rows * 2 * sizeof(float));
     P.desc = reinterpret_cast<PartDesc *>(w);
     void (*k)(AttnParams) = v.d == 576 && a.d_v == 512 ? attn_kernel<true>(v.fmt) : attn_kernel<false>(v.fmt);
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k, dim3((unsigned)ctas), dim3(kThreads), (size_t)kSmem, s, 1, P);
     if (e != cudaSuccess) return e;

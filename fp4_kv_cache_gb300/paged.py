@@ -1,26 +1,33 @@
 """Binding of the paged-cache calls of libcsa2.so (include/csa2_paged.h).
 
-As in ``csa2``: the ``csa2p_*`` functions mirror the C entry points, the short-named helpers
-allocate outputs with torch and call them, and everything is computed by the library's
-kernels.  Work goes to the current CUDA stream of the tensors' device (or the one given).
+As in ``csa2``: the helpers check what they are given, allocate outputs with torch and call the C
+entry points, and everything is computed by the library's kernels.  Work goes to the current
+CUDA stream (or the one given), on the current device, which has to be the tensors'.
+
+A decode step's calls take a few microseconds each on the GPU, so the way there is kept short:
+argument structures are packed with ``struct`` (the ctypes classes below name their fields and
+are checked against the C compiler's sizes in the tests).
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
 
 from . import csa2
-from .csa2 import _check
+from .csa2 import Csa2Error
 
 MXFP4, NVFP4_E4M3_16, MXFP8, BF16 = 0, 1, 2, 3
 DEV_NO_PAGES, DEV_TABLE_FULL, DEV_ROWS = 0x100, 0x200, 0x400
 MAX_BATCH = 16384
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_i32, _bf16, _f32 = torch.int32, torch.bfloat16, torch.float32
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class CacheArgs(ctypes.Structure):
@@ -49,6 +56,12 @@ class AttnArgs(ctypes.Structure):
                 ("lens", _P), ("cu", _P), ("pos0", _P), ("kv_start", _P)]
 
 
+_CACHE = "iii4xqPPqq"                                  # csa2p_cache
+_PLAN = struct.Struct("@5i4x11P")                      # csa2p_plan_args
+_ROPE = struct.Struct("@5i4xPPq")                      # csa2p_rope_axes
+_ATTN = struct.Struct("@" + _CACHE + "7if6P")          # csa2p_attn_args
+_CACHE = struct.Struct("@" + _CACHE)
+
 _ready = None
 
 
@@ -56,41 +69,53 @@ def _lib():
     global _ready
     if _ready is None:
         lib = csa2.load()
-        S, sz = ctypes.c_int, ctypes.c_size_t
+        S, sz, A = ctypes.c_int, ctypes.c_size_t, _P       # A: an argument structure
         for name, res, args in (
-                ("csa2p_page_plan", S, [ctypes.POINTER(PlanArgs), _P, _P]),
-                ("csa2p_rope", S, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _I32, ctypes.POINTER(RopeAxes), _P, _P]),
-                ("csa2p_write", S, [ctypes.POINTER(CacheArgs), _P, _I64, _I32, _P, ctypes.POINTER(RopeAxes), _P, _P]),
-                ("csa2p_read", S, [ctypes.POINTER(CacheArgs), _P, _I32, _P, _I64, _P, _P]),
-                ("csa2p_attn_workspace_size", sz, [ctypes.POINTER(AttnArgs)]),
-                ("csa2p_attn", S, [ctypes.POINTER(AttnArgs), _P, _P, _P, sz, _P, _P])):
+                ("csa2p_page_plan", S, [A, _P, _P]),
+                ("csa2p_rope", S, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _I32, A, _P, _P]),
+                ("csa2p_write", S, [A, _P, _I64, _I32, _P, A, _P, _P]),
+                ("csa2p_read", S, [A, _P, _I32, _P, _I64, _P, _P]),
+                ("csa2p_attn_workspace_size", sz, [A]),
+                ("csa2p_attn", S, [A, _P, _P, _P, sz, _P, _P])):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _ready = lib
     return _ready
 
 
-def _stream_of(t: torch.Tensor, stream):
-    """Raw stream of a call: the one given, else the current one of the tensor's device.  The
-    library works on the current device, so that has to be the tensor's."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {t.device}: make it the current device (torch.cuda.device)")
-    return (stream or torch.cuda.current_stream()).cuda_stream
+def _stream_of(dev: int, stream):
+    """Raw stream of a call on device `dev`: the one given, else the current one.  The library works
+    on the current device, so that has to be the tensors'."""
+    if dev != _device():
+        raise ValueError(f"the tensors are on cuda:{dev}: make it the current device (torch.cuda.device)")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, device=None):
-    """Address of a contiguous device tensor of this type (and shape), or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+def _bad(t, name: str, dtype, n: Optional[int], dev: int):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be on {device or 'the GPU'}, not {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be on {'the GPU' if dev < 0 else f'cuda:{dev}'}, not {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must hold {n} values, not {t.numel()} ({tuple(t.shape)})")
+
+
+def _need(t, name: str, dtype, n: Optional[int], dev: int) -> int:
+    """Address of a contiguous tensor of this type, size and device."""
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        _bad(t, name, dtype, n, dev)
     return t.data_ptr()
+
+
+def _maybe(t, name: str, dtype, n: Optional[int], dev: int) -> int:
+    return 0 if t is None else _need(t, name, dtype, n, dev)
+
+
+def _status(d_status, dev: int):
+    return None if d_status is None else _need(d_status, "d_status", _i32, None, dev)
 
 
 class PagedCache:
@@ -121,13 +146,16 @@ class PagedCache:
                 raise ValueError("rows must be contiguous within a page")
         self.codes, self.scales, self.fmt, self.d, self.page, self.n_pages = codes, scales, fmt, d, page, n
         self.device = codes.device
-        self.args = CacheArgs(fmt, d, page, n, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
-                              codes.stride(0) * codes.element_size() if n > 1 else 0,
-                              scales.stride(0) if scales is not None and n > 1 else 0)
+        self.index = codes.get_device()               # -1: not on a GPU
+        self.fields = (fmt, d, page, n, codes.data_ptr(), scales.data_ptr() if scales is not None else 0,
+                       codes.stride(0) * codes.element_size() if n > 1 else 0,
+                       scales.stride(0) if scales is not None and n > 1 else 0)
+        self.packed = _CACHE.pack(*self.fields)
 
-    def _on_gpu(self):
-        if not self.codes.is_cuda:
+    def _on_gpu(self) -> int:
+        if self.index < 0:
             raise ValueError("libcsa2 takes device tensors (got a CPU cache)")
+        return self.index
 
     @staticmethod
     def new(n_pages: int, page: int, d: int, fmt: int = MXFP4, device="cuda") -> "PagedCache":
@@ -150,67 +178,83 @@ class PagePlan:
     n_free: torch.Tensor      # [1] free pages left
 
 
-def csa2p_page_plan(args: PlanArgs, d_status=None, stream: int = 0):
-    _check("csa2p_page_plan", _lib().csa2p_page_plan(ctypes.byref(args), d_status, stream))
-
-
 def page_plan(lens, delta, block_table, free_pages, n_free, page: int, n_rows: int, in_place: bool = False,
               plan: Optional[PagePlan] = None, d_status=None, stream=None) -> PagePlan:
     """One step of the requests' bookkeeping: block_table [batch, width] and free_pages are updated,
     the rest is returned (into `plan`'s tensors when given).  in_place: lens and n_free are
-    overwritten with the new lengths and the new count, as a captured graph needs it."""
-    dev, B = lens.device, lens.shape[0]
+    overwritten with the new lengths and the new count, as a captured graph needs it.  See
+    csa2p_page_plan."""
+    dev, B = lens.get_device(), lens.shape[0]
+    width = block_table.shape[1]
     if plan is None:
-        buf = torch.empty(2 * B + 2 + 3 * n_rows, dtype=torch.int32, device=dev)
-        o = 2 * B + 2
-        plan = PagePlan(lens if in_place else buf[:B], buf[B:2 * B + 1], buf[o:o + n_rows], buf[o + n_rows:o + 2 * n_rows],
-                        buf[o + 2 * n_rows:], n_free if in_place else buf[2 * B + 1:o])
-    i32 = torch.int32
-    a = PlanArgs(B, page, block_table.shape[1], free_pages.shape[0], n_rows, _need(lens, "lens", i32, (B,), dev),
-                 _need(delta, "delta", i32, (B,), dev), _need(plan.lens, "plan.lens", i32, (B,), dev),
-                 _need(block_table, "block_table", i32, (B, block_table.shape[1]), dev),
-                 _need(free_pages, "free_pages", i32, (free_pages.shape[0],), dev), _need(n_free, "n_free", i32, (1,), dev),
-                 _need(plan.n_free, "plan.n_free", i32, (1,), dev), _need(plan.cu, "plan.cu", i32, (B + 1,), dev),
-                 _need(plan.slot, "plan.slot", i32, (n_rows,), dev), _need(plan.row_req, "plan.row_req", i32, (n_rows,), dev),
-                 _need(plan.row_pos, "plan.row_pos", i32, (n_rows,), dev))
-    csa2p_page_plan(a, _need(d_status, "d_status", i32, None, dev), _stream_of(lens, stream))
+        # one allocation: lens | n_free | cu | slot | row_req | row_pos
+        buf = torch.empty(2 * B + 2 + 3 * n_rows, dtype=_i32, device=lens.device)
+        parts = torch.split_with_sizes(buf, (B, 1, B + 1, n_rows, n_rows, n_rows))
+        base = buf.data_ptr()
+        at_cu, at_slot = base + 4 * B + 4, base + 8 * B + 8
+        if in_place:
+            plan = PagePlan(lens, parts[2], parts[3], parts[4], parts[5], n_free)
+            at_len, at_n = lens.data_ptr(), n_free.data_ptr()
+        else:
+            plan = PagePlan(parts[0], parts[2], parts[3], parts[4], parts[5], parts[1])
+            at_len, at_n = base, base + 4 * B
+        at_req, at_pos = at_slot + 4 * n_rows, at_slot + 8 * n_rows
+    else:
+        at_len, at_n = _need(plan.lens, "plan.lens", _i32, B, dev), _need(plan.n_free, "plan.n_free", _i32, 1, dev)
+        at_cu, at_slot = _need(plan.cu, "plan.cu", _i32, B + 1, dev), _need(plan.slot, "plan.slot", _i32, n_rows, dev)
+        at_req, at_pos = _need(plan.row_req, "plan.row_req", _i32, n_rows, dev), _need(plan.row_pos, "plan.row_pos", _i32, n_rows, dev)
+    a = _PLAN.pack(B, page, width, free_pages.shape[0], n_rows, _need(lens, "lens", _i32, B, dev),
+                   _need(delta, "delta", _i32, B, dev), at_len, _need(block_table, "block_table", _i32, B * width, dev),
+                   _need(free_pages, "free_pages", _i32, None, dev), _need(n_free, "n_free", _i32, 1, dev), at_n, at_cu, at_slot,
+                   at_req, at_pos)
+    st = (_ready or _lib()).csa2p_page_plan(a, _status(d_status, dev), _stream_of(dev, stream))
+    if st:
+        raise Csa2Error("csa2p_page_plan", st)
     return plan
 
 
-def _axes(pos, cos_sin, sections, rows: int, dev) -> Optional[RopeAxes]:
+def _axes(pos, cos_sin, sections, rows: int, dev: int):
     """csa2p_rope_axes of pos int32 [rows] or [axes, rows], cos_sin f32 [n_pos, rope_dim]; None: no
     rotation.  sections: pairs of each axis (one axis: all of them)."""
     if cos_sin is None:
         return None
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin is [n_pos, rope_dim]")
-    if pos is None or pos.shape[-1] != rows or pos.dim() not in (1, 2):
+    n = 1 if pos is None or pos.dim() == 1 else pos.shape[0]
+    if pos is None or pos.dim() not in (1, 2) or pos.shape[-1] != rows:
         raise ValueError("pos is [rows] or [axes, rows]")
-    n = pos.shape[0] if pos.dim() == 2 else 1
-    sections = [cos_sin.shape[1] // 2] if sections is None else sections
+    n_pos, dim = cos_sin.shape
+    sections = (dim // 2,) if sections is None else sections
     if len(sections) != n or n > 3:
         raise ValueError("sections gives the pairs of each of pos's one to three axes")
-    return RopeAxes(cos_sin.shape[1], n, (_I32 * 3)(*sections), _need(pos, "pos", torch.int32, None, dev),
-                    _need(cos_sin, "cos_sin", torch.float32, None, dev), cos_sin.shape[0])
+    sec = (*sections, 0, 0)
+    return _ROPE.pack(dim, n, sec[0], sec[1], sec[2], _need(pos, "pos", _i32, n * rows, dev),
+                      _need(cos_sin, "cos_sin", _f32, None, dev), n_pos)
 
 
 def rope_axes(x, pos, cos_sin, sections: Optional[Sequence[int]] = None, out=None, d_status=None, stream=None):
     """x bf16 [rows, heads, d] (strided over rows and heads) with its last rope_dim channels turned;
     out may be x.  See csa2p_rope."""
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or not x.is_cuda or x.stride(2) != 1:
+    dev = x.get_device()
+    if x.dim() != 3 or x.dtype is not _bf16 or dev < 0 or x.stride(2) != 1:
         raise ValueError("x is a bf16 device tensor [rows, heads, d] with contiguous channels")
     rows, heads, d = x.shape
+    sr, sh, _ = x.stride()
+    if rows < 2:                                       # a stride over one row or head means nothing
+        sr = heads * d
+    if heads < 2:
+        sh = d
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or out.stride(2) != 1:
-        raise ValueError("out must be like x")
-    r = _axes(pos, cos_sin, sections, rows, x.device)
-    # a stride over one row or one head only means nothing: the dense one stands in for it
-    strides = [(t.stride(0) if rows > 1 else heads * d, t.stride(1) if heads > 1 else d) for t in (x, out)]
-    _check("csa2p_rope", _lib().csa2p_rope(
-        x.data_ptr(), *strides[0], out.data_ptr(), *strides[1], rows, heads, d,
-        ctypes.byref(r) if r is not None else None, _need(d_status, "d_status", torch.int32, None, x.device),
-        _stream_of(x, stream)))
+        out = torch.empty((rows, heads, d), dtype=_bf16, device=x.device)
+        tr, th = heads * d, d
+    else:
+        if out.shape != x.shape or out.dtype is not _bf16 or out.get_device() != dev or out.stride(2) != 1:
+            raise ValueError("out must be like x")
+        tr, th = out.stride(0) if rows > 1 else heads * d, out.stride(1) if heads > 1 else d
+    st = (_ready or _lib()).csa2p_rope(x.data_ptr(), sr, sh, out.data_ptr(), tr, th, rows, heads, d,
+                                       _axes(pos, cos_sin, sections, rows, dev), _status(d_status, dev), _stream_of(dev, stream))
+    if st:
+        raise Csa2Error("csa2p_rope", st)
     return out
 
 
@@ -218,30 +262,32 @@ def paged_write(cache: PagedCache, x, slot, pos=None, cos_sin=None, sections: Op
                 d_status=None, stream=None):
     """Rows of x (bf16 [rows, d], rows may be strided) rotated (when cos_sin is given), quantised in
     the cache's format and stored at slot int32 [rows].  See csa2p_write."""
-    cache._on_gpu()
-    if x.dim() != 2 or x.dtype != torch.bfloat16 or x.device != cache.device or x.stride(1) != 1 or x.shape[1] != cache.d:
+    dev = cache._on_gpu()
+    if x.dim() != 2 or x.dtype is not _bf16 or x.get_device() != dev or x.stride(1) != 1 or x.shape[1] != cache.d:
         raise ValueError("x is a bf16 tensor [rows, d] on the cache's device with contiguous channels")
     rows = x.shape[0]
-    r = _axes(pos, cos_sin, sections, rows, x.device)
-    _check("csa2p_write", _lib().csa2p_write(
-        ctypes.byref(cache.args), x.data_ptr(), x.stride(0) if rows > 1 else cache.d, rows,
-        _need(slot, "slot", torch.int32, (rows,), x.device), ctypes.byref(r) if r is not None else None,
-        _need(d_status, "d_status", torch.int32, None, x.device), _stream_of(x, stream)))
+    st = (_ready or _lib()).csa2p_write(cache.packed, x.data_ptr(), x.stride(0) if rows > 1 else cache.d, rows,
+                                        _need(slot, "slot", _i32, rows, dev), _axes(pos, cos_sin, sections, rows, dev),
+                                        _status(d_status, dev), _stream_of(dev, stream))
+    if st:
+        raise Csa2Error("csa2p_write", st)
 
 
 def paged_read(cache: PagedCache, slot, out=None, d_status=None, stream=None):
     """bf16 [rows, d]: the cache rows of slot int32 [rows]; rows of a slot below 0 stay as they were
     (uninitialised in a new `out`).  See csa2p_read."""
-    cache._on_gpu()
-    rows = slot.shape[0]
+    dev = cache._on_gpu()
+    rows, d = slot.shape[0], cache.d
     if out is None:
-        out = torch.empty((rows, cache.d), dtype=torch.bfloat16, device=cache.device)
-    if out.dtype != torch.bfloat16 or out.device != cache.device or out.shape != (rows, cache.d) or out.stride(1) != 1:
-        raise ValueError("out is a bf16 tensor [rows, d] on the cache's device with contiguous channels")
-    _check("csa2p_read", _lib().csa2p_read(
-        ctypes.byref(cache.args), _need(slot, "slot", torch.int32, (rows,), cache.device), rows, out.data_ptr(),
-        out.stride(0) if rows > 1 else cache.d, _need(d_status, "d_status", torch.int32, None, cache.device),
-        _stream_of(out, stream)))
+        out, ldo = torch.empty((rows, d), dtype=_bf16, device=cache.device), d
+    else:
+        if out.dtype is not _bf16 or out.get_device() != dev or out.shape != (rows, d) or out.stride(1) != 1:
+            raise ValueError("out is a bf16 tensor [rows, d] on the cache's device with contiguous channels")
+        ldo = out.stride(0) if rows > 1 else d
+    st = (_ready or _lib()).csa2p_read(cache.packed, _need(slot, "slot", _i32, rows, dev), rows, out.data_ptr(), ldo,
+                                       _status(d_status, dev), _stream_of(dev, stream))
+    if st:
+        raise Csa2Error("csa2p_read", st)
     return out
 
 
@@ -252,33 +298,35 @@ def paged_attn(q, cache: PagedCache, block_table, lens, cu, pos0=None, d_v: Opti
     lse f32 [n_tokens, heads] or None).  q bf16 [n_tokens, heads, d]; block_table int32 [batch,
     width]; lens, pos0, kv_start int32 [batch]; cu int32 [batch + 1].  Rows of `out` and `lse`
     outside every request stay as they were.  See csa2p_attn."""
-    cache._on_gpu()
-    dev, lib, i32 = cache.device, _lib(), torch.int32
-    if q.dim() != 3 or q.shape[2] != cache.d:
-        raise ValueError("q is [n_tokens, heads, the cache's d]")
+    dev, lib = cache._on_gpu(), _ready or _lib()
+    if q.dim() != 3 or q.shape[2] != cache.d or block_table.dim() != 2:
+        raise ValueError("q is [n_tokens, heads, the cache's d], block_table [batch, width]")
     T, H, d = q.shape
     d_v = d if d_v is None else d_v
-    B = lens.shape[0]
-    if block_table.dim() != 2:
-        raise ValueError("block_table is [batch, width]")
-    W = block_table.shape[1]
-    a = AttnArgs(cache.args, B, T, H, d_v, W, window, ratio_m, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale,
-                 _need(q, "q", torch.bfloat16, None, dev), _need(block_table, "block_table", i32, (B, W), dev),
-                 _need(lens, "lens", i32, (B,), dev), _need(cu, "cu", i32, (B + 1,), dev), _need(pos0, "pos0", i32, (B,), dev),
-                 _need(kv_start, "kv_start", i32, (B,), dev))
+    B, W = lens.shape[0], block_table.shape[1]
+    a = _ATTN.pack(*cache.fields, B, T, H, d_v, W, window, ratio_m, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale,
+                   _need(q, "q", _bf16, None, dev), _need(block_table, "block_table", _i32, B * W, dev),
+                   _need(lens, "lens", _i32, B, dev), _need(cu, "cu", _i32, B + 1, dev), _maybe(pos0, "pos0", _i32, B, dev),
+                   _maybe(kv_start, "kv_start", _i32, B, dev))
+    at_out = _maybe(out, "out", _bf16, T * H * max(d_v, 0), dev)
     if out is None:
-        out = torch.empty((T, H, max(d_v, 0)), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H, max(d_v, 0)), dtype=_bf16, device=cache.device)
+        at_out = out.data_ptr()
+    at_lse = _maybe(lse, "lse", _f32, T * H, dev)
     if lse is None and want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    ref = ctypes.byref(a)
-    need = lib.csa2p_attn_workspace_size(ref)
-    raw = _stream_of(q, stream)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        lse = torch.empty((T, H), dtype=_f32, device=cache.device)
+        at_lse = lse.data_ptr()
+    need = lib.csa2p_attn_workspace_size(a)
+    raw = _stream_of(dev, stream)
+    at_ws, size = 0, 0
+    if workspace is not None:
+        at_ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        at_ws, size = workspace.data_ptr(), need
         if stream is not None:
             workspace.record_stream(stream)
-    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("csa2p_attn", lib.csa2p_attn(
-        ref, _need(out, "out", torch.bfloat16, (T, H, d_v), dev), _need(lse, "lse", torch.float32, (T, H), dev),
-        workspace.data_ptr() if workspace is not None else None, size, _need(d_status, "d_status", i32, None, dev), raw))
+    st = lib.csa2p_attn(a, at_out, at_lse or None, at_ws or None, size, _status(d_status, dev), raw)
+    if st:
+        raise Csa2Error("csa2p_attn", st)
     return out, lse

@@ -173,7 +173,7 @@ def test_formats_from_widths():
         assert (c.fmt, c.d, c.page, c.n_pages) == (fmt, 576, 16, 3)
     wide = torch.zeros((6, 2, 16, 288), dtype=torch.uint8)                 # two layers' pages side by side
     c = paged.PagedCache(wide[:, 1], torch.zeros((6, 16, 18), dtype=torch.uint8))
-    assert c.args.code_stride == 2 * 16 * 288 and c.args.scale_stride == 16 * 18
+    assert c.fields[-2:] == (2 * 16 * 288, 16 * 18)
 
 
 def test_binding_refuses(lib):
@@ -198,6 +198,23 @@ def test_binding_refuses(lib):
                         torch.zeros(4, dtype=i32), torch.zeros(1, dtype=i32), 16, 4)
     with pytest.raises(ValueError):
         paged.rope_axes(torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=i32), torch.zeros((9, 32)))
+
+
+def test_packed_structures():
+    # the packed argument structures lie as the ctypes (and so the C) ones do
+    for packer, cls in ((paged._CACHE, paged.CacheArgs), (paged._PLAN, paged.PlanArgs), (paged._ROPE, paged.RopeAxes),
+                        (paged._ATTN, paged.AttnArgs)):
+        assert packer.size == ctypes.sizeof(cls)
+    c = paged.PagedCache.new(3, 16, 576, paged.NVFP4_E4M3_16, device="cpu")
+    a = paged.CacheArgs.from_buffer_copy(c.packed)
+    assert [getattr(a, n) or 0 for n, _ in a._fields_] == list(c.fields)
+    v = list(range(1, 17))
+    a = paged.PlanArgs.from_buffer_copy(paged._PLAN.pack(*v))
+    assert [getattr(a, n) for n, _ in a._fields_] == v
+    a = paged.RopeAxes.from_buffer_copy(paged._ROPE.pack(*v[:8]))
+    assert (a.rope_dim, a.n_axes, list(a.section), a.pos, a.cos_sin, a.n_pos) == (1, 2, [3, 4, 5], 6, 7, 8)
+    a = paged.AttnArgs.from_buffer_copy(paged._ATTN.pack(*c.fields, *v[:7], 0.5, *v[8:14]))
+    assert [getattr(a, n) for n, _ in a._fields_[1:]] == v[:7] + [0.5] + v[8:14]
 
 
 def test_status_text():
