@@ -4,15 +4,14 @@
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
-
-#include <cuda_bf16.h>
+#include "paged_decode.cuh"
 
 namespace csa2 {
 namespace {
 
 // ---------------------------------------------------------------- bookkeeping
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanCluster = 8;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxReq = CSA2P_MAX_BATCH / kPlanThreads;     // requests a thread
 
 struct PlanParams {
     int32_t batch, shift, width, free_cap, n_rows;
@@ -55,13 +54,13 @@ __device__ __forceinline__ int last_at_or_below(const int32_t *a, int n, int32_t
 
 __device__ __forceinline__ int32_t hold31(int64_t v) { return (int32_t)(v > 0x7fffffff ? 0x7fffffff : v); }
 
-// One launch: every CTA (one, or a cluster of eight when there are many rows) scans all the
-// requests for itself -- rows added, pages taken, pages given back -- so that the rows, the
-// taken pages and the returned pages can then be shared out with no further exchange.  What
-// another CTA may still read (lens, n_free) is overwritten only after a cluster barrier; table
-// entries read are never written here (a request takes or gives back, not both), and the free
-// list is read below n_free and written above it.
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams P, uint32_t *d_status)
+// Every CTA scans all the requests for itself -- rows added, pages taken, pages given back -- so
+// that the rows, the taken pages and the returned pages can be shared out with no exchange.  No
+// CTA writes what another may still read: table entries read are never written (a request takes or
+// gives back, not both), and the free list is read below n_free and written above it.  Only the new
+// lengths and count may go where the old ones are: then (`later`) a second kernel writes them, and
+// with one CTA a barrier is enough.
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams P, const int later, uint32_t *d_status)
 {
     extern __shared__ int32_t sm[];
     int32_t *s_cu = sm, *s_take = s_cu + P.batch + 1, *s_back = s_take + P.batch + 1;
@@ -70,6 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     const int n_cta = gridDim.x, cta = blockIdx.x;
     pdl_wait();
     pdl_allow_dependents();
+    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
     // ---- scan of the requests, `per` consecutive ones a thread
     const int per = (P.batch + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     __syncthreads();
     if (warp < 3) {
-        int64_t v = s_warp[warp][lane];
+        int64_t v = lane < kPlanThreads / 32 ? s_warp[warp][lane] : 0;
         const int64_t mine = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -121,7 +121,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     __syncthreads();
     const int n_new = s_cu[P.batch], n_take = s_take[P.batch], n_back = s_back[P.batch];
-    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
     const int64_t top = (int64_t)n_free + n_back;
     if (tid == 0 && cta == 0) {
         if (n_take > top) dev_flag(d_status, CSA2P_DEV_NO_PAGES);
@@ -179,44 +178,127 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     const int64_t left = top - n_take < 0 ? 0 : top - n_take;
     for (int64_t i = first; i < n_back; i += step)
         if (n_free + i < left && n_free + i < P.free_cap) P.free_pages[n_free + i] = returned((int)i);
-    int32_t len_new[16];                                       // per <= CSA2P_MAX_BATCH / 1024
-    if (cta == 0)
+    if (later || cta > 0) return;
+    int32_t len_new[kPlanMaxReq];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (b0 + k < b1) len_new[k] = (int32_t)plan_req(P, b0 + k).new_len;
-    if (n_cta > 1)
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else
-        __syncthreads();
-    if (cta == 0) {
+    for (int k = 0; k < kPlanMaxReq; ++k)
+        if (b0 + k < b1) len_new[k] = (int32_t)plan_req(P, b0 + k).new_len;
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (b0 + k < b1) P.lens_out[b0 + k] = len_new[k];
-        if (tid == 0) P.n_free_out[0] = (int32_t)(left < P.free_cap ? left : P.free_cap);
+    for (int k = 0; k < kPlanMaxReq; ++k)
+        if (b0 + k < b1) P.lens_out[b0 + k] = len_new[k];
+    if (tid == 0) P.n_free_out[0] = (int32_t)(left < P.free_cap ? left : P.free_cap);
+}
+
+// The new lengths and count, when they overwrite the old ones: one block, all read before any is
+// written.  The count follows from the pages that the requests take and give back.
+__global__ void __launch_bounds__(kPlanThreads) page_plan_later_kernel(const PlanParams P)
+{
+    __shared__ int64_t s_warp[kPlanThreads / 32];
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_allow_dependents();
+    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
+    int64_t grown = 0;
+    int32_t len_new[kPlanMaxReq];
+#pragma unroll
+    for (int k = 0; k < kPlanMaxReq; ++k) {
+        const int b = tid + k * kPlanThreads;
+        if (b < P.batch) {
+            const Req r = plan_req(P, b);
+            len_new[k] = (int32_t)r.new_len;
+            grown += r.has - r.had;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) grown += __shfl_xor_sync(0xffffffffu, grown, o);
+    if ((tid & 31) == 0) s_warp[tid >> 5] = grown;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPlanMaxReq; ++k) {
+        const int b = tid + k * kPlanThreads;
+        if (b < P.batch) P.lens_out[b] = len_new[k];
+    }
+    if (tid == 0) {
+        int64_t left = n_free;
+        for (int w = 0; w < kPlanThreads / 32; ++w) left -= s_warp[w];
+        P.n_free_out[0] = (int32_t)(left < 0 ? 0 : left < P.free_cap ? left : P.free_cap);
     }
 }
 
 // ---------------------------------------------------------------- rotation
 // Turns the pairs of eight channels col .. col+7 that lie at or past channel c0 (even), with
-// one rounding per product and per sum, as csa2_rope_quant_fp4 does.
-__device__ __forceinline__ void rotate8(float (&v)[8], int col, int c0, const RopeView &R, int64_t row, int64_t rows,
-                                        uint32_t *d_status)
+// one rounding per product and per sum, as csa2_rope_quant_fp4 does.  at[]: the row's positions.
+struct Positions { int32_t at[3]; };
+__device__ __forceinline__ Positions row_positions(const RopeView &R, int64_t row, int64_t rows)
 {
     const int half = R.dim >> 1;
+    Positions p;
+    p.at[0] = R.pos[row];
+    p.at[1] = R.end0 < half ? R.pos[rows + row] : -1;
+    p.at[2] = R.end1 < half ? R.pos[2 * rows + row] : -1;
+    return p;
+}
+__device__ __forceinline__ void rotate8(float (&v)[8], int col, int c0, const RopeView &R, const Positions &at, uint32_t *d_status)
+{
+    const int half = R.dim >> 1;
+    float c[4], s[4];
+    bool on[4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const int i = (col + e - c0) >> 1;
-        if (col + e < c0) continue;
-        const int axis = (i >= R.end0) + (i >= R.end1);
-        const int64_t p = R.pos[axis * rows + row];
-        if (p < 0) continue;
+    for (int k = 0; k < 4; ++k) {                 // all on their way before the first is used
+        const int i = (col + 2 * k - c0) >> 1;
+        int32_t p = i < R.end0 ? at.at[0] : i < R.end1 ? at.at[1] : at.at[2];
+        if (col + 2 * k < c0) p = -1;
         if (p >= R.n_pos) {
             dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-            continue;
+            p = -1;
         }
-        const float c = R.cs[p * R.dim + i], s = R.cs[p * R.dim + half + i], a = v[e], b = v[e + 1];
-        v[e] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-        v[e + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+        on[k] = p >= 0;
+        const float *cs = R.cs + (int64_t)p * R.dim + i;
+        c[k] = on[k] ? cs[0] : 1.0f;
+        s[k] = on[k] ? cs[half] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float a = v[2 * k], b = v[2 * k + 1];
+        if (on[k]) {
+            v[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+            v[2 * k + 1] = __fadd_rn(__fmul_rn(a, s[k]), __fmul_rn(b, c[k]));
+        }
+    }
+}
+
+// The same where four pairs share an axis and lie aligned (RopeView.quads): position, then cosines
+// and sines 16 bytes at a time, so that a kernel can have them on their way with its rows.
+struct Turn {
+    int32_t p;          // position, or -1: nothing to turn
+    float4 c, s;
+};
+__device__ __forceinline__ int32_t turn_position(const RopeView &R, int col, int c0, int64_t row, int64_t rows)
+{
+    const int i = (col - c0) >> 1;
+    return R.pos[((i >= R.end0) + (i >= R.end1)) * rows + row];
+}
+__device__ __forceinline__ void turn_load(Turn &t, const RopeView &R, int col, int c0, uint32_t *d_status)
+{
+    if (t.p >= R.n_pos) {
+        dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        t.p = -1;
+    }
+    if (t.p < 0) return;
+    const float *cs = R.cs + (int64_t)t.p * R.dim + ((col - c0) >> 1);
+    t.c = *reinterpret_cast<const float4 *>(cs);
+    t.s = *reinterpret_cast<const float4 *>(cs + (R.dim >> 1));
+}
+__device__ __forceinline__ void turn8(float (&v)[8], const Turn &t)
+{
+    if (t.p < 0) return;
+    const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float a = v[2 * k], b = v[2 * k + 1];
+        v[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+        v[2 * k + 1] = __fadd_rn(__fmul_rn(a, s[k]), __fmul_rn(b, c[k]));
     }
 }
 
@@ -246,7 +328,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8])
 // turned channels are visited.
 __global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *__restrict__ x, int64_t x_row, int64_t x_head,
                                                          uint16_t *out, int64_t out_row, int64_t out_head, int32_t heads,
-                                                         int32_t d, int32_t first_piece, int64_t rows, const RopeView R,
+                                                         int32_t d, int32_t first_piece, int64_t rows,
+                                                         const __grid_constant__ RopeView R,
                                                          uint32_t *d_status)
 {
     pdl_wait();
@@ -259,7 +342,14 @@ __global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *__restr
         if (R.dim > 0 && col + 8 > c0) {
             float v[8];
             unpack8(raw, v);
-            rotate8(v, col, c0, R, row, rows, d_status);
+            if (R.quads) {
+                Turn t;
+                t.p = turn_position(R, col, c0, row, rows);
+                turn_load(t, R, col, c0, d_status);
+                turn8(v, t);
+            } else {
+                rotate8(v, col, c0, R, row_positions(R, row, rows), d_status);
+            }
             raw = pack8(v);
         }
         *reinterpret_cast<uint4 *>(out + row * out_row + h * out_head + col) = raw;
@@ -267,131 +357,193 @@ __global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *__restr
 }
 
 // ---------------------------------------------------------------- write
-// A lane takes eight channels of one row (16 bytes of x); the lanes of a scale block are
-// neighbours (4 for 32 channels, 2 for 16; d is a multiple of 32, so none straddles a row).
-template <int FMT>
-__global__ void __launch_bounds__(256) paged_write_kernel(const PagedView C, const uint16_t *__restrict__ x, int64_t ldx,
-                                                          int32_t rows, const int32_t *__restrict__ slot,
-                                                          const RopeView R, uint32_t *d_status)
+__device__ __forceinline__ float max_nan(float a, float b)      // NaN if either is
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Blocks of (d / 16, rows) threads: thread (x, y) takes sixteen channels of a row (32 bytes of x),
+// a scale block of 32 channels is two neighbours of one warp (d / 16 is even).  What bounds it is
+// its instructions, about as many for the addresses and the scale as for eight channels: with
+// eight channels a thread 16,384 rows of 576 took 9.7 us (MXFP4, no rotation).
+// ROPE 0: none; 1: RopeView.quads; 2: any.
+template <int FMT, int ROPE>
+__global__ void __launch_bounds__(1024) paged_write_kernel(const PagedView C, const uint16_t *__restrict__ x, int64_t ldx,
+                                                           int32_t rows, const int32_t *__restrict__ slot,
+                                                           const __grid_constant__ RopeView R, uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
-    const int lanes = C.d / 8, c0 = C.d - R.dim;
-    const int64_t total = (int64_t)rows * lanes, total32 = (total + 31) & ~int64_t(31);
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total32; t += (int64_t)gridDim.x * 256) {
-        const int64_t r = t < total ? t / lanes : 0;
-        const int sub8 = t < total ? (int)(t - r * lanes) : 0, col = 8 * sub8;
-        const int32_t sl = t < total ? slot[r] : -1;
-        const bool act = sl >= 0 && sl < C.n_slots;
-        if (sl >= C.n_slots) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        float v[8];
-        if (act) {
-            unpack8(*reinterpret_cast<const uint4 *>(x + r * ldx + col), v);
-            if (R.dim > 0 && col + 8 > c0) rotate8(v, col, c0, R, r, rows, d_status);
-        } else {
+    const int part = threadIdx.x, col = 16 * part, c0 = C.d - R.dim;
+    // whole blocks go round together: the threads of a warp stay with each other's shuffles
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < rows; r0 += (int64_t)gridDim.x * blockDim.y) {
+        const int64_t r = r0 + threadIdx.y;
+        const bool in = r < rows;
+        const int32_t sl = in ? slot[r] : -1;
+        uint4 raw[2] = {};
+        Turn turn[2] = {{-1, {}, {}}, {-1, {}, {}}};
+        Positions at = {};
+        if (in) {
+            raw[0] = reinterpret_cast<const uint4 *>(x + r * ldx + col)[0];
+            raw[1] = reinterpret_cast<const uint4 *>(x + r * ldx + col)[1];
+            if (ROPE == 2 && col + 16 > c0) at = row_positions(R, r, rows);
+            if (ROPE == 1 && col + 16 > c0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+                for (int h = 0; h < 2; ++h)
+                    if (col + 8 * h >= c0) turn[h].p = turn_position(R, col + 8 * h, c0, r, rows);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) turn_load(turn[h], R, col + 8 * h, c0, sl >= 0 ? d_status : nullptr);
+            }
         }
-        uint8_t *codes = const_cast<uint8_t *>(C.codes) + C.code_at(act ? sl : 0);
+        const bool act = sl >= 0 && sl < C.n_slots;
+        if (sl >= C.n_slots && part == 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        float e[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            unpack8(raw[h], e[h]);
+            if (ROPE == 1) turn8(e[h], turn[h]);
+            if (ROPE == 2 && act && col + 8 * h + 8 > c0) rotate8(e[h], col + 8 * h, c0, R, at, d_status);
+        }
+        uint8_t *codes = const_cast<uint8_t *>(C.codes) + C.code_at(act ? sl : 0) + part * code_bytes<FMT>(16);
         if (FMT == CSA2P_BF16) {
-            if (act) *reinterpret_cast<uint4 *>(codes + 2 * col) = pack8(v);
+            if (act) {
+                reinterpret_cast<uint4 *>(codes)[0] = pack8(e[0]);
+                reinterpret_cast<uint4 *>(codes)[1] = pack8(e[1]);
+            }
             continue;
         }
-        uint32_t amax = 0;
+        float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        if (FMT != CSA2P_NVFP4_E4M3_16) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(e[i >> 3][i & 7]));
+        if (FMT != CSA2P_NVFP4_E4M3_16) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         if (!act) continue;
-        const bool head = (sub8 & (FMT == CSA2P_NVFP4_E4M3_16 ? 1 : 3)) == 0, finite = amax < 0x7f800000u;
-        if (!finite && head) dev_flag(d_status, CSA2_DEV_NONFINITE);
-        const float amax_f = __uint_as_float(finite ? amax : 0u);
+        const bool head = FMT == CSA2P_NVFP4_E4M3_16 || (part & 1) == 0;
+        if (!(amax < INFINITY)) {
+            if (head) dev_flag(d_status, CSA2_DEV_NONFINITE);
+            amax = 0.0f;
+        }
         uint32_t sbyte;
         if (FMT == CSA2P_MXFP8) {
-            const int X = mx8_block_exponent(amax_f);
+            const int X = mx8_block_exponent(amax);
             const float inv = pow2_neg(X);
-            uint32_t w[2] = {0u, 0u};
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i >> 2] |= e4m3_cvt(v[i] * inv) << (8 * (i & 3));
-            *reinterpret_cast<uint2 *>(codes + col) = make_uint2(w[0], w[1]);
+            for (int i = 0; i < 16; ++i) w[i >> 2] |= e4m3_cvt(e[i >> 3][i & 7] * inv) << (8 * (i & 3));
+            *reinterpret_cast<uint4 *>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
             sbyte = (uint32_t)(X + 127);
         } else {
-            uint32_t word = 0;
+            uint32_t w[2] = {0u, 0u};
             if (FMT == CSA2P_NVFP4_E4M3_16) {
-                sbyte = e4m3_block_scale(amax_f);
+                sbyte = e4m3_block_scale(amax);
                 const float sc = e4m3_value(sbyte);
                 if (sc > 0.0f) {
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2)
-                        word |= e2m1x2_cvt(__fdiv_rn(v[i], sc), __fdiv_rn(v[i + 1], sc)) << (4 * i);
+                    for (int i = 0; i < 16; i += 2)
+                        w[i >> 3] |= e2m1x2_cvt(__fdiv_rn(e[i >> 3][i & 7], sc), __fdiv_rn(e[i >> 3][(i & 7) + 1], sc)) << (4 * (i & 7));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) word |= (__float_as_uint(v[i]) >> 31) << (4 * i + 3);
+                    for (int i = 0; i < 16; ++i) w[i >> 3] |= (__float_as_uint(e[i >> 3][i & 7]) >> 31) << (4 * (i & 7) + 3);
                 }
             } else {
-                const int X = mx_block_exponent(amax_f);
+                const int X = mx_block_exponent(amax);
                 const float inv = pow2_neg(X);
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) word |= e2m1x2_cvt(v[i] * inv, v[i + 1] * inv) << (4 * i);
+                for (int i = 0; i < 16; i += 2)
+                    w[i >> 3] |= e2m1x2_cvt(e[i >> 3][i & 7] * inv, e[i >> 3][(i & 7) + 1] * inv) << (4 * (i & 7));
                 sbyte = (uint32_t)(X + 127);
             }
-            *reinterpret_cast<uint32_t *>(codes + col / 2) = word;
+            *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
         }
-        if (head)
-            const_cast<uint8_t *>(C.scales)[C.scale_at(sl) + col / (FMT == CSA2P_NVFP4_E4M3_16 ? 16 : 32)] = (uint8_t)sbyte;
+        if (head) const_cast<uint8_t *>(C.scales)[C.scale_at(sl) + (FMT == CSA2P_NVFP4_E4M3_16 ? part : part >> 1)] = (uint8_t)sbyte;
     }
 }
 
 // ---------------------------------------------------------------- read
+// Sixteen channels with a scale that one product cannot apply, or not finite: code x scale in
+// float32 (exact), rounded to bf16 once.
 template <int FMT>
-__global__ void __launch_bounds__(256) paged_read_kernel(const PagedView C, const int32_t *__restrict__ slot, int32_t rows,
-                                                         uint16_t *__restrict__ out, int64_t ldo, uint32_t *d_status)
+__device__ __noinline__ void read_slow(Raw<FMT, 2> r, uint16_t *to)
 {
-    pdl_wait();
-    pdl_allow_dependents();
-    const int lanes = C.d / 8;
-    const int64_t total = (int64_t)rows * lanes;
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-        const int64_t r = t / lanes;
-        const int col = 8 * (int)(t - r * lanes);
-        const int32_t sl = slot[r];
-        if (sl < 0) continue;
-        if (sl >= C.n_slots) {
-            dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-            continue;
-        }
-        const uint8_t *codes = C.codes + C.code_at(sl);
-        uint4 o;
-        if (FMT == CSA2P_BF16) {
-            o = *reinterpret_cast<const uint4 *>(codes + 2 * col);
+    const float sc = FMT == CSA2P_NVFP4_E4M3_16 ? e4m3_value(r.sb & 0xffu)
+                     : r.sb == 255u ? __uint_as_float(0x7fc00000u) : e8m0_value(r.sb);
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+        float x;
+        if (FMT == CSA2P_MXFP8) {
+            x = e4m3_value((r.w[(e >> 2) % Raw<FMT, 2>::kWords] >> (8 * (e & 3))) & 0xffu);
         } else {
-            const uint32_t sb = C.scales[C.scale_at(sl) + col / (FMT == CSA2P_NVFP4_E4M3_16 ? 16 : 32)];
-            // code x scale is exact in float32 and rounded to bf16 once
-            const float sc = FMT == CSA2P_NVFP4_E4M3_16 ? e4m3_value(sb)
-                             : sb == 255u ? __uint_as_float(0x7fc00000u) : e8m0_value(sb);
-            float v[8];
-            if (FMT == CSA2P_MXFP8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(codes + col);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = e4m3_value(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu) * sc;
-            } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + col / 2);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t c = (w >> (4 * i)) & 15u;
-                    v[i] = (c & 8u ? -e2m1_mag(c & 7u) : e2m1_mag(c & 7u)) * sc;
-                }
-            }
-            o = pack8(v);
+            const uint32_t c = (r.w[(e >> 3) % Raw<FMT, 2>::kWords] >> (4 * (e & 7))) & 15u;
+            x = c & 8u ? -e2m1_mag(c & 7u) : e2m1_mag(c & 7u);
         }
-        *reinterpret_cast<uint4 *>(out + r * ldo + col) = o;
+        to[e] = __bfloat16_as_ushort(__float2bfloat16_rn(x * sc));
     }
 }
 
-int blocks_for(int64_t threads, int per_sm)
+// Sixteen channels a thread, U rows at once.
+template <int FMT, int U>
+__global__ void __launch_bounds__(1024) paged_read_kernel(const PagedView C, const int32_t *__restrict__ slot, int32_t rows,
+                                                         uint16_t *__restrict__ out, int64_t ldo, uint32_t f0, uint32_t f4,
+                                                         uint32_t *d_status)
 {
-    const int64_t g = (threads + 255) / 256, most = (int64_t)device_sm_count() * per_sm;
-    return (int)(g < 1 ? 1 : g > most ? most : g);
+    pdl_wait();
+    pdl_allow_dependents();
+    const int part = threadIdx.x;
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y * U; r0 < rows; r0 += (int64_t)gridDim.x * blockDim.y * U) {
+        int32_t sls[U];
+        Raw<FMT, 2> raw[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t r = r0 + k * blockDim.y + threadIdx.y;
+            sls[k] = r < rows ? slot[r] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (sls[k] >= C.n_slots) {
+                if (part == 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+                sls[k] = -1;
+            }
+            if (sls[k] >= 0)
+                load_raw(raw[k], C.codes + C.code_at(sls[k]) + part * code_bytes<FMT>(16),
+                         C.scales + C.scale_at(sls[k]) + (FMT == CSA2P_NVFP4_E4M3_16 ? part : part >> 1));
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (sls[k] < 0) continue;
+            uint16_t *to = out + (r0 + k * blockDim.y + threadIdx.y) * ldo + 16 * part;
+            if (FMT != CSA2P_BF16 && unusual(raw[k])) {
+                read_slow(raw[k], to);
+                continue;
+            }
+            uint32_t v[8];
+            if (FMT == CSA2P_BF16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = raw[k].w[i % Raw<FMT, 2>::kWords];
+            } else {
+                uint32_t p[8];
+                decode(raw[k], p, f0, f4);
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {          // channels 0 4, 1 5, 2 6, 3 7 into order
+                    v[h] = prmt(p[h], p[h + 1], 0x5410u);
+                    v[h + 1] = prmt(p[h + 2], p[h + 3], 0x5410u);
+                    v[h + 2] = prmt(p[h], p[h + 1], 0x7632u);
+                    v[h + 3] = prmt(p[h + 2], p[h + 3], 0x7632u);
+                }
+            }
+            reinterpret_cast<uint4 *>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4 *>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+// Threads (d / 16, rows a block: a multiple of 16, so whole warps) and blocks of the write and read
+// kernels.
+dim3 row_block(int32_t d) { return dim3((unsigned)(d / 16), (unsigned)(16 * (d < 256 ? 256 / d : 1))); }
+unsigned row_grid(int32_t d, int64_t rows)
+{
+    const int64_t by = row_block(d).y, g = (rows + by - 1) / by, most = (int64_t)device_sm_count() * 8;
+    return (unsigned)(g > most ? most : g);
 }
 
 } // namespace
@@ -449,8 +601,14 @@ cudaError_t launch_page_plan(const csa2p_plan_args &a, uint32_t *d_status, cudaS
         const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const int ctas = a.n_rows > 4 * kPlanThreads ? kPlanCluster : 1;
-    return launch_pdl(page_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, s, (unsigned)ctas, P, d_status);
+    // four rows a thread; few rows: one CTA, which needs no second kernel
+    int64_t ctas = ((int64_t)a.n_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    if (ctas < 1) ctas = 1;
+    if (ctas > device_sm_count()) ctas = device_sm_count();
+    const bool later = ctas > 1 && (a.lens_out == a.lens || a.n_free_out == a.n_free);
+    const cudaError_t e = launch_pdl(page_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, s, 1, P, later ? 1 : 0, d_status);
+    if (e != cudaSuccess || !later) return e;
+    return launch_pdl(page_plan_later_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, P);
 }
 
 cudaError_t launch_paged_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_t *out, int64_t out_row,
@@ -470,21 +628,21 @@ cudaError_t launch_paged_rope(const uint16_t *x, int64_t x_row, int64_t x_head, 
 cudaError_t launch_paged_write(const PagedView &v, const uint16_t *x, int64_t ldx, int32_t rows, const int32_t *slot,
                                const RopeView &rope, uint32_t *d_status, cudaStream_t s)
 {
-    const int g = blocks_for((int64_t)rows * (v.d / 8), 16);
-    auto k = v.fmt == CSA2P_MXFP4 ? paged_write_kernel<CSA2P_MXFP4>
-             : v.fmt == CSA2P_NVFP4_E4M3_16 ? paged_write_kernel<CSA2P_NVFP4_E4M3_16>
-             : v.fmt == CSA2P_MXFP8 ? paged_write_kernel<CSA2P_MXFP8> : paged_write_kernel<CSA2P_BF16>;
-    return launch_pdl(k, dim3(g), dim3(256), 0, s, 1, v, x, ldx, rows, slot, rope, d_status);
+#define CSA2P_PICK(K, N) (v.fmt == CSA2P_MXFP4 ? K<CSA2P_MXFP4, N> : v.fmt == CSA2P_NVFP4_E4M3_16 ? K<CSA2P_NVFP4_E4M3_16, N> \
+                          : v.fmt == CSA2P_MXFP8 ? K<CSA2P_MXFP8, N> : K<CSA2P_BF16, N>)
+    auto k = rope.dim == 0 ? CSA2P_PICK(paged_write_kernel, 0) : rope.quads ? CSA2P_PICK(paged_write_kernel, 1) : CSA2P_PICK(paged_write_kernel, 2);
+    return launch_pdl(k, dim3(row_grid(v.d, rows)), row_block(v.d), 0, s, 1, v, x, ldx, rows, slot, rope, d_status);
 }
 
 cudaError_t launch_paged_read(const PagedView &v, const int32_t *slot, int32_t rows, uint16_t *out, int64_t ldo,
                               uint32_t *d_status, cudaStream_t s)
 {
-    const int g = blocks_for((int64_t)rows * (v.d / 8), 16);
-    auto k = v.fmt == CSA2P_MXFP4 ? paged_read_kernel<CSA2P_MXFP4>
-             : v.fmt == CSA2P_NVFP4_E4M3_16 ? paged_read_kernel<CSA2P_NVFP4_E4M3_16>
-             : v.fmt == CSA2P_MXFP8 ? paged_read_kernel<CSA2P_MXFP8> : paged_read_kernel<CSA2P_BF16>;
-    return launch_pdl(k, dim3(g), dim3(256), 0, s, 1, v, slot, rows, out, ldo, d_status);
+    // one row a thread while there are few, two once they fill the GPU
+    const bool two = rows >= (int64_t)device_sm_count() * row_block(v.d).y * 2;
+    auto k = two ? CSA2P_PICK(paged_read_kernel, 2) : CSA2P_PICK(paged_read_kernel, 1);
+#undef CSA2P_PICK
+    return launch_pdl(k, dim3(row_grid(v.d, two ? (rows + 1) / 2 : rows)), row_block(v.d), 0, s, 1, v, slot, rows, out, ldo, kCodeAt0,
+                      kCodeAt4, d_status);
 }
 
 } // namespace csa2

@@ -31,6 +31,7 @@ struct RopeView {
     const float *cs;
     int64_t n_pos;
     int32_t dim, end0, end1;           // rotated channels; pairs below end0 take axis 0, below end1 axis 1
+    int32_t quads;                     // every four pairs of eight channels share an axis and lie aligned
 };
 
 bool paged_view(const csa2p_cache &c, PagedView &v);    // false: not a valid cache

@@ -18,7 +18,7 @@ inline bool pow2_page(int32_t p) { return p >= 1 && p <= 65536 && (p & (p - 1)) 
 // false: not a valid rotation of rows of d channels
 bool rope_view(const csa2p_rope_axes *r, int32_t d, RopeView &v)
 {
-    v = {nullptr, nullptr, 0, 0, 0, 0};
+    v = {nullptr, nullptr, 0, 0, 0, 0, 0};
     if (!r || r->rope_dim == 0) return true;
     if (r->rope_dim < 0 || r->rope_dim % 2 || r->rope_dim > d) return false;
     if (r->n_axes < 1 || r->n_axes > 3) return false;
@@ -35,7 +35,7 @@ bool rope_view(const csa2p_rope_axes *r, int32_t d, RopeView &v)
     v.dim = r->rope_dim;
     v.end0 = r->section[0];
     v.end1 = r->n_axes > 1 ? r->section[0] + r->section[1] : r->section[0];
-    if (r->n_axes == 1) v.end1 = v.end0;
+    v.quads = (d - v.dim) % 8 == 0 && v.dim % 8 == 0 && v.end0 % 4 == 0 && v.end1 % 4 == 0 && aligned(r->cos_sin, 16);
     return true;
 }
 
