@@ -254,9 +254,13 @@ __device__ __forceinline__ void rotate8(float (&v)[8], int col, int c0, const Ro
             p = -1;
         }
         on[k] = p >= 0;
-        const float *cs = R.cs + (int64_t)p * R.dim + i;
-        c[k] = on[k] ? cs[0] : 1.0f;
-        s[k] = on[k] ? cs[half] : 0.0f;
+        c[k] = 1.0f;
+        s[k] = 0.0f;
+        if (on[k]) {
+            const float *cs = R.cs + (int64_t)p * R.dim + i;
+            c[k] = cs[0];
+            s[k] = cs[half];
+        }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
