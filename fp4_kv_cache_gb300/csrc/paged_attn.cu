@@ -39,7 +39,6 @@ namespace {
 
 constexpr int kThreads = 640;           // warps 0-7 softmax, 8 MMA, 9-19 staging
 constexpr int kMmaWarp = 8, kStageWarp = 9, kStageWarps = 11, kStageThreads = 32 * kStageWarps;
-constexpr int kTasks = 6;               // staging tasks of 32 channels a warp and tile, at most
 constexpr int kRing = 3;                // tiles whose rows are looked up: this one and two ahead
 constexpr int kRows = 64, kKeys = 128;
 constexpr int kQUnit = 8192;            // 64 rows x 64 dims of bf16, 128-byte swizzle
@@ -382,36 +381,59 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (warp >= kStageWarp) {
         // ============================================================ staging
         // Task (chunk pair, 8 keys): lane (key, q) decodes the q-th scale block of 32 channels of
-        // the pair; eight lanes of a store hold eight keys, hence eight different columns.  Warp w
-        // takes tasks w, w + 11, ..; chunk 8 makes 16 tasks of half the size, spread so that each
-        // warp has about the same.  A task's registers are loaded for the next tile as soon as they
-        // are decoded, so a whole tile's rows are on their way from memory.
-        const int w = warp - kStageWarp, k7 = lane & 7, q = lane >> 3;
+        // the pair.  A key's four lanes read 64 bytes of its row; so that eight lanes of a store hold
+        // eight different columns, the second chunk's blocks start with their upper half.  Warp w
+        // takes tasks w, w + 11, .., two at a time with one fence; chunk 8 makes 16 tasks of half the
+        // size, spread so that each warp has about the same.  The next two tasks' rows are always on
+        // their way.  The loops stay rolled: the roles' code together has to fit the instruction
+        // cache (unrolled over a tile's six tasks, a quarter of all issue slots waited for code).
+        const int w = warp - kStageWarp, key8 = lane >> 2, q = lane & 3;
+        const bool swap = q >= 2;
         const int j0 = w < 9 ? 6 + w : 3 * (w - 9), jn = w < 9 ? (w == 0 ? 2 : 1) : 3, jstep = w < 9 ? 9 : 1;
         const int lane_code = q * code_bytes<FMT>(32), lane_scale = FMT == CSA2P_NVFP4_E4M3_16 ? 2 * q : q;
-        const int place = kOffK + (q >> 1) * kChunk + k7 * 128;
+        const int place = kOffK + (q >> 1) * kChunk + key8 * 128;
         int col[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) col[i] = ((4 * (q & 1) + i) ^ k7) << 4;
+        for (int i = 0; i < 4; ++i) col[i] = ((4 * (q & 1) + (i ^ (swap ? 2 : 0))) ^ key8) << 4;
         bool ok = true;
-        // how many of its tasks a warp has loaded ahead (registers)
-        constexpr int kAhead = FMT == CSA2P_BF16 ? 2 : FMT == CSA2P_MXFP8 ? 3 : kTasks;
         auto live = [&](int task) { return task < 64 && (FULL || (task >> 4) < pairs); };
         auto load_task = [&](Raw<FMT, 4> &r, int ring, int task) {
-            const RowAt a = M.row[ring][8 * (task & 15) + k7];
+            const RowAt a = M.row[ring][8 * (task & 15) + key8];
             const int cp = task >> 4;
             if (a.code != nullptr && (FULL || 4 * cp + q < n_blocks))
                 load_raw(r, a.code + lane_code + cp * code_bytes<FMT>(128), a.scale + lane_scale + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
             else
                 zero_raw(r);
         };
-        Raw<FMT, 4> raw[kAhead];
+        int freed = 4;                                // last block of the tile before known to be done
+        auto store_task = [&](Raw<FMT, 4> &r, uint32_t n, int task) {
+            const int kg = task & 15, cp = task >> 4;
+            uint32_t v[16];
+            swap_raw(r, swap);
+            decode(r, v, P.f0, P.f4);
+            const int need = min(cp, n_pv - 1);
+            if (freed < need) {
+                ok = wait_bar(&M.pv_done[need], (n - 1) & 1, &M.abort) && ok;
+                freed = need;
+            }
+            uint8_t *u = sm + place + cp * 2 * kChunk + kg * 1024;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (unusual(r)) decode_slow(r, u, col[0], 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
+        };
+        // two tasks in hand, two on their way
+        Raw<FMT, 4> a0, a1, b0, b1;
+        auto load_two = [&](Raw<FMT, 4> &x, Raw<FMT, 4> &y, int ring, int task) {
+            if (live(task)) load_task(x, ring, task);
+            if (live(task + kStageWarps)) load_task(y, ring, task + kStageWarps);
+        };
         if (units > 0) {
             ok = wait_bar(&M.rows[0], 0, &M.abort);
-            if (ok)
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (live(w + kStageWarps * k)) load_task(raw[k], 0, w + kStageWarps * k);
+            if (ok) {
+                load_two(a0, a1, 0, w);
+                load_two(b0, b1, 0, w + 2 * kStageWarps);
+            }
         }
         int ring = 0;                                 // n mod kRing, and the parity of the ring's round
         uint32_t round = 0;
@@ -438,63 +460,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
             }
             if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
-            int freed = n > 0 ? -1 : 4;               // last block of the tile before known to be done
-#pragma unroll
-            for (int k = 0; k < kTasks; ++k) {
-                const int task = w + kStageWarps * k;
-                if (!live(task)) continue;
-                const int kg = task & 15, cp = task >> 4;
-                Raw<FMT, 4> &r = raw[k % kAhead];
-                uint32_t v[16];
-                decode(r, v, P.f0, P.f4);
-                const int need = min(cp, n_pv - 1);
-                if (freed < need) {
-                    ok = wait_bar(&M.pv_done[need], (n - 1) & 1, &M.abort) && ok;
-                    freed = need;
-                }
-                uint8_t *u = sm + place + cp * 2 * kChunk + kg * 1024;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (unusual(r)) decode_slow(r, u, col[0], 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + k7));
+            freed = n > 0 ? -1 : 4;
+            const int rounds = FULL ? 3 : (16 * pairs + 2 * kStageWarps - 1) / (2 * kStageWarps);
+#pragma unroll 1
+            for (int k = 0; k < rounds; ++k) {
+                const int task = w + 2 * kStageWarps * k;
+                if (live(task)) store_task(a0, n, task);
+                if (live(task + kStageWarps)) store_task(a1, n, task + kStageWarps);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&M.full_k[cp]);
-                // the registers' next task: later in this tile, or in the next
-                if (k + kAhead < kTasks) {
-                    if (live(task + kStageWarps * kAhead)) load_task(r, ring, task + kStageWarps * kAhead);
-                } else if (more) {
-                    const int t1 = w + kStageWarps * ((k + kAhead) % kTasks);
-                    if (live(t1)) load_task(r, ring1, t1);
+                if (lane == 0) {
+                    if (live(task)) tc::mbar_arrive(&M.full_k[task >> 4]);
+                    if (live(task + kStageWarps)) tc::mbar_arrive(&M.full_k[(task + kStageWarps) >> 4]);
                 }
+                a0 = b0;
+                a1 = b1;
+                const int k2 = k + 2 < rounds ? k + 2 : k + 2 - rounds;     // two rounds on, maybe of the next tile
+                if (k + 2 < rounds || more) load_two(b0, b1, k + 2 < rounds ? ring : ring1, w + 2 * kStageWarps * k2);
             }
             if (tail) {
                 Raw<FMT, 2> r8[3];
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     if (i >= jn) break;
-                    const RowAt a = M.row[ring][8 * (j0 + i * jstep) + k7];
+                    const RowAt a = M.row[ring][8 * (j0 + i * jstep) + key8];
                     if (a.code != nullptr && (FULL || 16 + (q >> 1) < n_blocks))
                         load_raw(r8[i], a.code + lane_code / 2 + code_bytes<FMT>(512), a.scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
                     else
                         zero_raw(r8[i]);
                 }
                 if (n > 0) ok = wait_bar(&M.pv_done[n_pv - 1], (n - 1) & 1, &M.abort) && ok;
+                const int c8 = ((2 * q) ^ key8) << 4;
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     if (i >= jn) break;
                     const int kg = j0 + i * jstep;
                     uint32_t v[8];
                     decode(r8[i], v, P.f0, P.f4);
-                    uint8_t *u = sm + kOffP + kg * 1024 + k7 * 128;
-                    const int c8 = ((2 * q) ^ k7) << 4;
+                    uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
                     *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
-                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + k7));
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&M.full_k[4]);
+                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
                 }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    for (int i = 0; i < jn; ++i) tc::mbar_arrive(&M.full_k[4]);
             }
             ring = ring1;
             round = round1;
@@ -512,20 +523,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             int ring = 0;
 #pragma unroll 1
             for (uint32_t n = 0; n < (uint32_t)units; ++n) {
-#pragma unroll
-                for (int g = 0; g < 5; ++g) {
-                    if (2 * g >= chunks) break;
-                    ok = wait_bar(&M.full_k[g], n & 1, &M.abort);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = 2 * g + i;
-                        if (c < 9 && c < chunks)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma(tmem, dk + c * (kChunk / 16) + k * 2, dq + c * (kQUnit / 16) + k * 2, instr(0, 0), (c | k) != 0);
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    if ((c & 1) == 0) {
+                        ok = wait_bar(&M.full_k[c >> 1], n & 1, &M.abort);
+                        if (!ok) break;
+                        tc::tc_fence_after();
                     }
+                    const uint64_t a = dk + (uint32_t)(c * (kChunk / 16)), b = dq + (uint32_t)(c * (kQUnit / 16));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma(tmem, a + k * 2, b + k * 2, instr(0, 0), (c | k) != 0);
                 }
                 if (!ok) break;
                 const bool first = (M.tile[ring].flags & kFirst) != 0;   // read before the softmax may go on
@@ -534,12 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 ok = wait_bar(&M.full_p, n & 1, &M.abort);
                 if (!ok) break;
                 tc::tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < n_pv; ++j) {
+                    const uint64_t a = dv + (uint32_t)(j * (2 * kChunk / 16));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j >= n_pv) break;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma(tmem + 64 + 64 * j, dv + j * (2 * kChunk / 16) + k * 128, dp + k * 128, instr(1, 1), !(first && k == 0));
+                    for (int k = 0; k < 8; ++k) mma(tmem + 64 + 64 * j, a + k * 128, dp + k * 128, instr(1, 1), !(first && k == 0));
                     tc::tc_commit(&M.pv_done[j]);
                 }
             }

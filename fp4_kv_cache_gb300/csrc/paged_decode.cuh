@@ -79,6 +79,20 @@ __device__ __forceinline__ void zero_raw(Raw<FMT, N> &r)
     for (int i = 0; i < Raw<FMT, N>::kWords; ++i) r.w[i] = 0u;
     r.sb = FMT == CSA2P_NVFP4_E4M3_16 ? 0u : 127u;
 }
+// Swaps the two halves of the channels, when `swap`.
+template <int FMT, int N>
+__device__ __forceinline__ void swap_raw(Raw<FMT, N> &r, bool swap)
+{
+    constexpr int kH = Raw<FMT, N>::kWords / 2;
+#pragma unroll
+    for (int i = 0; i < kH; ++i) {
+        const uint32_t a = r.w[i], b = r.w[i + kH];
+        r.w[i] = swap ? b : a;
+        r.w[i + kH] = swap ? a : b;
+    }
+    if (FMT == CSA2P_NVFP4_E4M3_16 && N == 4) r.sb = swap ? prmt(r.sb, 0u, 0x4401u) : r.sb;
+}
+
 // Whether these channels need decode_slow: scales that one product cannot apply, and what is not
 // finite.
 template <int FMT, int N>
