@@ -101,11 +101,20 @@ struct AttnParams {
 };
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The descriptors' upper words do not change: a product's two operands are told by their lower
+// ones (the address and the leading offset).
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ float ex2(float x)
 {
@@ -383,10 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // Task (chunk pair, 8 keys): lane (key, q) decodes the q-th scale block of 32 channels of
         // the pair.  A key's four lanes read 64 bytes of its row; so that eight lanes of a store hold
         // eight different columns, the second chunk's blocks start with their upper half.  Warp w
-        // takes tasks w, w + 11, .., two at a time with one fence; chunk 8 makes 16 tasks of half the
-        // size, spread so that each warp has about the same.  The next two tasks' rows are always on
-        // their way.  The loops stay rolled: the roles' code together has to fit the instruction
-        // cache (unrolled over a tile's six tasks, a quarter of all issue slots waited for code).
+        // takes tasks w, w + 11, .., three a round: a round is one run of instructions with nothing
+        // to wait for inside, one fence at its end (72 tasks with MMAs beside them took 2,770 cycles
+        // with six tasks a round, 3,750 with two).  Chunk 8 makes 16 tasks of half the size, spread so
+        // that each warp has about the same.  A round's rows of the next tile are on their way as
+        // soon as its registers are free; where they lie is read before it starts.
         const int w = warp - kStageWarp, key8 = lane >> 2, q = lane & 3;
         const bool swap = q >= 2;
         const int j0 = w < 9 ? 6 + w : 3 * (w - 9), jn = w < 9 ? (w == 0 ? 2 : 1) : 3, jstep = w < 9 ? 9 : 1;
@@ -396,43 +406,63 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < 4; ++i) col[i] = ((4 * (q & 1) + (i ^ (swap ? 2 : 0))) ^ key8) << 4;
         bool ok = true;
+        constexpr bool kDeep = FMT == CSA2P_MXFP4 || FMT == CSA2P_NVFP4_E4M3_16;   // registers for a tile ahead
         auto live = [&](int task) { return task < 64 && (FULL || (task >> 4) < pairs); };
-        auto load_task = [&](Raw<FMT, 4> &r, int ring, int task) {
-            const RowAt a = M.row[ring][8 * (task & 15) + key8];
+        auto load_task = [&](Raw<FMT, 4> &r, const RowAt &a, int task) {
             const int cp = task >> 4;
-            if (a.code != nullptr && (FULL || 4 * cp + q < n_blocks))
+            if (a.code != nullptr && live(task) && (FULL || 4 * cp + q < n_blocks))
                 load_raw(r, a.code + lane_code + cp * code_bytes<FMT>(128), a.scale + lane_scale + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
             else
                 zero_raw(r);
         };
-        int freed = 4;                                // last block of the tile before known to be done
-        auto store_task = [&](Raw<FMT, 4> &r, uint32_t n, int task) {
-            const int kg = task & 15, cp = task >> 4;
-            uint32_t v[16];
-            swap_raw(r, swap);
-            decode(r, v, P.f0, P.f4);
-            const int need = min(cp, n_pv - 1);
-            if (freed < need) {
-                ok = wait_bar(&M.pv_done[need], (n - 1) & 1, &M.abort) && ok;
-                freed = need;
-            }
-            uint8_t *u = sm + place + cp * 2 * kChunk + kg * 1024;
+        auto where = [&](RowAt (&a)[3], int ring, int k0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (unusual(r)) decode_slow(r, u, col[0], 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
+            for (int k = 0; k < 3; ++k) a[k] = M.row[ring][8 * ((w + kStageWarps * (k0 + k)) & 15) + key8];
         };
-        // two tasks in hand, two on their way
-        Raw<FMT, 4> a0, a1, b0, b1;
-        auto load_two = [&](Raw<FMT, 4> &x, Raw<FMT, 4> &y, int ring, int task) {
-            if (live(task)) load_task(x, ring, task);
-            if (live(task + kStageWarps)) load_task(y, ring, task + kStageWarps);
+        auto load_round = [&](Raw<FMT, 4> (&r)[3], const RowAt (&a)[3], int k0) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) load_task(r[k], a[k], w + kStageWarps * (k0 + k));
         };
+        auto store_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n, int k0) {
+            // the chunks have been left by the product before: blocks are done in order
+            const int last = min(w + kStageWarps * (k0 + 2), 63);
+            if (n > 0) ok = wait_bar(&M.pv_done[min(min(last >> 4, pairs - 1), n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
+            bool odd[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const int task = w + kStageWarps * (k0 + k);
+                uint32_t v[16];
+                swap_raw(r[k], swap);
+                decode(r[k], v, P.f0, P.f4);
+                odd[k] = unusual(r[k]) && live(task);
+                uint8_t *u = sm + place + (task >> 4) * 2 * kChunk + (task & 15) * 1024;
+                if (live(task))
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            if (odd[0] || odd[1] || odd[2]) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int task = w + kStageWarps * (k0 + k), kg = task & 15;
+                    if (odd[k])
+                        decode_slow(r[k], sm + place + (task >> 4) * 2 * kChunk + kg * 1024, col[0], 16, &M.nan[n & 1][kg >> 2],
+                                    1u << (8 * (kg & 3) + key8));
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane < 3 && live(w + kStageWarps * (k0 + lane))) tc::mbar_arrive(&M.full_k[(w + kStageWarps * (k0 + lane)) >> 4]);
+        };
+        Raw<FMT, 4> ra[3], rb[3];
+        RowAt at[3];
         if (units > 0) {
             ok = wait_bar(&M.rows[0], 0, &M.abort);
-            if (ok) {
-                load_two(a0, a1, 0, w);
-                load_two(b0, b1, 0, w + 2 * kStageWarps);
+            if (ok && kDeep) {
+                where(at, 0, 0);
+                load_round(ra, at, 0);
+                where(at, 0, 3);
+                load_round(rb, at, 3);
             }
         }
         int ring = 0;                                 // n mod kRing, and the parity of the ring's round
@@ -460,23 +490,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
             }
             if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
-            freed = n > 0 ? -1 : 4;
-            const int rounds = FULL ? 3 : (16 * pairs + 2 * kStageWarps - 1) / (2 * kStageWarps);
+            if (kDeep) {
+                where(at, ring1, 0);                  // stale where there is no next tile: not used
+                store_round(ra, n, 0);
+                if (more) load_round(ra, at, 0);
+                where(at, ring1, 3);
+                store_round(rb, n, 3);
+                if (more) load_round(rb, at, 3);
+            } else {
 #pragma unroll 1
-            for (int k = 0; k < rounds; ++k) {
-                const int task = w + 2 * kStageWarps * k;
-                if (live(task)) store_task(a0, n, task);
-                if (live(task + kStageWarps)) store_task(a1, n, task + kStageWarps);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (live(task)) tc::mbar_arrive(&M.full_k[task >> 4]);
-                    if (live(task + kStageWarps)) tc::mbar_arrive(&M.full_k[(task + kStageWarps) >> 4]);
+                for (int k0 = 0; k0 < 6; k0 += 3) {
+                    where(at, ring, k0);
+                    load_round(ra, at, k0);
+                    store_round(ra, n, k0);
                 }
-                a0 = b0;
-                a1 = b1;
-                const int k2 = k + 2 < rounds ? k + 2 : k + 2 - rounds;     // two rounds on, maybe of the next tile
-                if (k + 2 < rounds || more) load_two(b0, b1, k + 2 < rounds ? ring : ring1, w + 2 * kStageWarps * k2);
             }
             if (tail) {
                 Raw<FMT, 2> r8[3];
@@ -512,46 +539,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         }
         if (!ok) M.abort = 1;
     } else if (warp == kMmaWarp) {
-        // ============================================================ MMA (one thread)
-        if (lane == 0) {
-            const uint32_t base = tc::smem_u32(sm);
-            const uint64_t dq = tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
-            const uint64_t dk = tc::smem_desc(base + kOffK, 16, 1024, tc::kSwizzle128B);
-            const uint64_t dv = tc::smem_desc(base + kOffK, kChunk, 1024, tc::kSwizzle128B);
-            const uint64_t dp = tc::smem_desc(base + kOffP, kChunk, 1024, tc::kSwizzle128B);
-            bool ok = true;
-            int ring = 0;
+        // ============================================================ MMA
+        // The whole warp goes through the loops, so that what they compute is the same for all of it
+        // and stays in uniform registers; one thread issues.  (With one thread in the loops each MMA
+        // took over 100 cycles to issue beside five busy warps, 48 to run.)
+        const uint32_t base = tc::smem_u32(sm);
+        const uint64_t dk = tc::smem_desc(base + kOffK, 16, 1024, tc::kSwizzle128B);
+        const uint64_t dv = tc::smem_desc(base + kOffK, kChunk, 1024, tc::kSwizzle128B);
+        const uint32_t upper = (uint32_t)(dk >> 32);      // stride, version, swizzle: the same for all
+        const uint32_t k_lo = (uint32_t)dk, v_lo = (uint32_t)dv, q_lo = (uint32_t)tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
+        const uint32_t p_lo = (uint32_t)tc::smem_desc(base + kOffP, kChunk, 1024, tc::kSwizzle128B);
+        bool ok = true;
+        int ring = 0;
 #pragma unroll 1
-            for (uint32_t n = 0; n < (uint32_t)units; ++n) {
+        for (uint32_t n = 0; n < (uint32_t)units; ++n) {
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    if ((c & 1) == 0) {
-                        ok = wait_bar(&M.full_k[c >> 1], n & 1, &M.abort);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                    }
-                    const uint64_t a = dk + (uint32_t)(c * (kChunk / 16)), b = dq + (uint32_t)(c * (kQUnit / 16));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma(tmem, a + k * 2, b + k * 2, instr(0, 0), (c | k) != 0);
+            for (int c = 0; c < chunks; ++c) {
+                if ((c & 1) == 0) {
+                    ok = __all_sync(0xffffffffu, wait_bar(&M.full_k[c >> 1], n & 1, &M.abort));
+                    if (!ok) break;
+                    tc::tc_fence_after();
                 }
-                if (!ok) break;
-                const bool first = (M.tile[ring].flags & kFirst) != 0;   // read before the softmax may go on
-                ring = ring == kRing - 1 ? 0 : ring + 1;
-                tc::tc_commit(&M.s_done);
-                ok = wait_bar(&M.full_p, n & 1, &M.abort);
-                if (!ok) break;
-                tc::tc_fence_after();
+                const uint32_t a = k_lo + c * (kChunk / 16), b = q_lo + c * (kQUnit / 16), first = c != 0;
+                if (elect_one()) {
+                    mma(tmem, a, b, upper, instr(0, 0), first);
+                    mma(tmem, a + 2, b + 2, upper, instr(0, 0), 1);
+                    mma(tmem, a + 4, b + 4, upper, instr(0, 0), 1);
+                    mma(tmem, a + 6, b + 6, upper, instr(0, 0), 1);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            const uint32_t later = (M.tile[ring].flags & kFirst) == 0;   // read before the softmax may go on
+            ring = ring == kRing - 1 ? 0 : ring + 1;
+            if (elect_one()) tc::tc_commit(&M.s_done);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, wait_bar(&M.full_p, n & 1, &M.abort));
+            if (!ok) break;
+            tc::tc_fence_after();
 #pragma unroll 1
-                for (int j = 0; j < n_pv; ++j) {
-                    const uint64_t a = dv + (uint32_t)(j * (2 * kChunk / 16));
+            for (int j = 0; j < n_pv; ++j) {
+                const uint32_t a = v_lo + j * (2 * kChunk / 16), d = tmem + 64 + 64 * j;
+                if (elect_one()) {
+                    mma(d, a, p_lo, upper, instr(1, 1), later);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) mma(tmem + 64 + 64 * j, a + k * 128, dp + k * 128, instr(1, 1), !(first && k == 0));
+                    for (int k = 1; k < 8; ++k) mma(d, a + k * 128, p_lo + k * 128, upper, instr(1, 1), 1);
                     tc::tc_commit(&M.pv_done[j]);
                 }
+                __syncwarp();
             }
-            if (!ok) M.abort = 1;
-            tc::tc_commit(&M.drained);                // nothing may still run when the CTA leaves
         }
+        if (!ok) M.abort = 1;
+        if (elect_one()) tc::tc_commit(&M.drained);       // nothing may still run when the CTA leaves
         __syncwarp();
     } else {
         // ============================================================ softmax and output
