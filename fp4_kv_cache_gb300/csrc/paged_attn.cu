@@ -50,7 +50,6 @@ constexpr float kUnset = 1e30f;         // -maximum of a row that has seen no ke
 // shared memory: Q 9 units | chunks 0..7 | chunk 8, or P^T once S has been computed | the rest
 constexpr int kOffK = 9 * kQUnit, kOffP = kOffK + 8 * kChunk, kOffMisc = kOffP + kChunk;
 
-struct RowAt { const uint8_t *code, *scale; };   // a key's row; code NULL: no key
 struct TileAt {                          // a key tile, for everyone
     int64_t row0;                        // its row tile: first row in q, rows, place in lo and hi
     int32_t rows, item;
@@ -65,7 +64,7 @@ constexpr uint32_t kTail = 8, kPart = 16;     // the row tile began in a CTA bef
 struct Misc {
     uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
     uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
-    RowAt row[kRing][kKeys];
+    int32_t slot[kRing][kKeys];         // a key's row of the cache; -1: no key
     TileAt tile[kRing];
     float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
     float red[4][kRows];
@@ -89,6 +88,7 @@ struct PartDesc {        // per CTA: the row tile it starts and does not finish
 struct AttnParams {
     PagedView C;
     int32_t batch, n_tokens, H, d_v, width, window, ratio, chunks, n_pv;
+    int32_t dense;                // pages follow one another
     float log2_scale;
     uint32_t f0, f4;              // see decode
     const uint16_t *q;
@@ -408,20 +408,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         bool ok = true;
         constexpr bool kDeep = FMT == CSA2P_MXFP4 || FMT == CSA2P_NVFP4_E4M3_16;   // registers for a tile ahead
         auto live = [&](int task) { return task < 64 && (FULL || (task >> 4) < pairs); };
-        auto load_task = [&](Raw<FMT, 4> &r, const RowAt &a, int task) {
+        const uint8_t *codes = P.C.codes + lane_code, *scales = P.C.scales + lane_scale;
+        // where a row lies: dense pages follow one another
+        auto code_of = [&](int32_t sl) -> const uint8_t * { return codes + (P.dense ? (int64_t)sl * P.C.code_row : P.C.code_at(sl)); };
+        auto scale_of = [&](int32_t sl) -> const uint8_t * { return scales + (P.dense ? (int64_t)sl * P.C.scale_row : P.C.scale_at(sl)); };
+        auto load_task = [&](Raw<FMT, 4> &r, int32_t sl, int task) {
             const int cp = task >> 4;
-            if (a.code != nullptr && live(task) && (FULL || 4 * cp + q < n_blocks))
-                load_raw(r, a.code + lane_code + cp * code_bytes<FMT>(128), a.scale + lane_scale + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
+            if (sl >= 0 && live(task) && (FULL || 4 * cp + q < n_blocks))
+                load_raw(r, code_of(sl) + cp * code_bytes<FMT>(128), scale_of(sl) + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
             else
                 zero_raw(r);
         };
-        auto where = [&](RowAt (&a)[3], int ring, int k0) {
+        auto where = [&](int32_t (&a)[6], int ring) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) a[k] = M.row[ring][8 * ((w + kStageWarps * (k0 + k)) & 15) + key8];
+            for (int k = 0; k < 6; ++k) a[k] = M.slot[ring][8 * ((w + kStageWarps * k) & 15) + key8];
         };
-        auto load_round = [&](Raw<FMT, 4> (&r)[3], const RowAt (&a)[3], int k0) {
+        auto load_round = [&](Raw<FMT, 4> (&r)[3], const int32_t (&a)[6], int k0) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) load_task(r[k], a[k], w + kStageWarps * (k0 + k));
+            for (int k = 0; k < 3; ++k) load_task(r[k], a[k0 + k], w + kStageWarps * (k0 + k));
+        };
+        Raw<FMT, 2> r8[3];                            // chunk 8
+        auto load_tail = [&](int ring) {
+            // lane q takes channels 512 + 16 q ..; codes and scales are offset by lane_code, lane_scale
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if (i >= jn) break;
+                const int32_t sl = M.slot[ring][8 * (j0 + i * jstep) + key8];
+                if (sl >= 0 && (FULL || 16 + (q >> 1) < n_blocks))
+                    load_raw(r8[i], code_of(sl) - lane_code / 2 + code_bytes<FMT>(512),
+                             scale_of(sl) - lane_scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
+                else
+                    zero_raw(r8[i]);
+            }
         };
         auto store_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n, int k0) {
             // the chunks have been left by the product before: blocks are done in order
@@ -455,13 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (lane < 3 && live(w + kStageWarps * (k0 + lane))) tc::mbar_arrive(&M.full_k[(w + kStageWarps * (k0 + lane)) >> 4]);
         };
         Raw<FMT, 4> ra[3], rb[3];
-        RowAt at[3];
+        int32_t at[6];
         if (units > 0) {
             ok = wait_bar(&M.rows[0], 0, &M.abort);
             if (ok && kDeep) {
-                where(at, 0, 0);
+                where(at, 0);
                 load_round(ra, at, 0);
-                where(at, 0, 3);
                 load_round(rb, at, 3);
             }
         }
@@ -491,31 +508,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             }
             if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
             if (kDeep) {
-                where(at, ring1, 0);                  // stale where there is no next tile: not used
+                if (tail) load_tail(ring);
+                where(at, ring1);                     // stale where there is no next tile: not used
                 store_round(ra, n, 0);
                 if (more) load_round(ra, at, 0);
-                where(at, ring1, 3);
                 store_round(rb, n, 3);
                 if (more) load_round(rb, at, 3);
             } else {
-#pragma unroll 1
-                for (int k0 = 0; k0 < 6; k0 += 3) {
-                    where(at, ring, k0);
-                    load_round(ra, at, k0);
-                    store_round(ra, n, k0);
-                }
+                where(at, ring);
+                load_round(ra, at, 0);
+                store_round(ra, n, 0);
+                load_round(ra, at, 3);
+                store_round(ra, n, 3);
+                if (tail) load_tail(ring);
             }
             if (tail) {
-                Raw<FMT, 2> r8[3];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    if (i >= jn) break;
-                    const RowAt a = M.row[ring][8 * (j0 + i * jstep) + key8];
-                    if (a.code != nullptr && (FULL || 16 + (q >> 1) < n_blocks))
-                        load_raw(r8[i], a.code + lane_code / 2 + code_bytes<FMT>(512), a.scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
-                    else
-                        zero_raw(r8[i]);
-                }
                 if (n > 0) ok = wait_bar(&M.pv_done[n_pv - 1], (n - 1) & 1, &M.abort) && ok;
                 const int c8 = ((2 * q) ^ key8) << 4;
 #pragma unroll
@@ -604,18 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // rows' bounds.
         auto look = [&]() {
             const int32_t key0 = walk.key0(), k = key0 + key_in;
-            RowAt a = {nullptr, nullptr};
+            int32_t sl = -1;
             if (k >= walk.it.lo && k < walk.it.hi) {
                 const int32_t id = P.table[(int64_t)walk.it.b * P.width + (k >> P.C.shift)];
-                if (id >= 0 && id < P.C.n_pages) {
-                    const int32_t sl = (int32_t)(((uint32_t)id << P.C.shift) + (k & ((1 << P.C.shift) - 1)));
-                    a.code = P.C.codes + P.C.code_at(sl);
-                    a.scale = P.C.scales + P.C.scale_at(sl);
-                } else {
-                    dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
-                }
+                if (id >= 0 && id < P.C.n_pages) sl = (int32_t)(((uint32_t)id << P.C.shift) + (k & ((1 << P.C.shift) - 1)));
+                else dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
             }
-            M.row[ahead_ring][key_in] = a;
+            M.slot[ahead_ring][key_in] = sl;
             if (walk.first()) {
                 ++ib;
                 if (key_in < kRows) {                 // rows past the last: as the last
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             failed |= __any_sync(0xffffffffu, !wait_bar(&M.rows[ring], round, &M.abort));
             const TileAt &T = M.tile[ring];
             const uint32_t flags = T.flags;
-            const bool first = flags & kFirst, have = M.row[ring][key_in].code != nullptr;
+            const bool first = flags & kFirst, have = M.slot[ring][key_in] >= 0;
             if (first) {
                 if (half == 0 && key_in < kRows) {
                     M.m[key_in] = -INFINITY;
@@ -681,11 +683,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 look();
                 more = walk.next(P);
             }
-            failed |= __any_sync(0xffffffffu, !wait_bar(&M.full_k[tail ? 4 : pairs - 1], ph, &M.abort) || !wait_bar(&M.s_done, ph, &M.abort));
-            tc::tc_fence_after();
+            failed |= __any_sync(0xffffffffu, !wait_bar(&M.full_k[tail ? 4 : pairs - 1], ph, &M.abort));
             const bool nan = (M.nan[ph][quad] >> lane) & 1u;
+            const bool masked = (flags & kEdge) || __any_sync(0xffffffffu, nan || !have);
+            failed |= __any_sync(0xffffffffu, !wait_bar(&M.s_done, ph, &M.abort));
+            tc::tc_fence_after();
             // ---- logits that a row does not see become -inf, those of a key that is not finite NaN
-            if ((flags & kEdge) || __any_sync(0xffffffffu, nan || !have)) {
+            if (masked) {
                 const int32_t key = T.key0 + key_in, item = T.item;
 #pragma unroll 1
                 for (int c0 = 0; c0 < 32; c0 += 16) {
@@ -973,6 +977,7 @@ cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint
     P.chunks = (v.d + 63) / 64;
     P.n_pv = (a.d_v + 127) / 128;
     P.log2_scale = a.sm_scale * 1.4426950408889634f;
+    P.dense = v.code_page == (int64_t)v.code_row << v.shift && v.scale_page == (int64_t)v.scale_row << v.shift;
     P.f0 = kCodeAt0;
     P.f4 = kCodeAt4;
     P.q = a.q;
