@@ -47,6 +47,8 @@ csa2_status attn_check(const csa2p_attn_args *a, PagedView &v)
     if (a->n_heads < 1 || a->n_heads > 128) return CSA2_ERR_INVALID_ARG;
     if (a->d_v < 8 || a->d_v % 8 || a->d_v > v.d) return CSA2_ERR_INVALID_ARG;
     if (v.d > 576 || a->d_v > 512) return CSA2_ERR_UNSUPPORTED;
+    // the kernel tells rows by 32-bit offsets: codes in 16 bytes, scales in bytes
+    if (v.code_page * v.n_pages >= (int64_t(1) << 36) || v.scale_page * v.n_pages >= (int64_t(1) << 32)) return CSA2_ERR_UNSUPPORTED;
     if (a->width < 0 || a->window < 0 || a->ratio_m < 1) return CSA2_ERR_INVALID_ARG;
     if (!(a->sm_scale > 0.0f) || a->sm_scale > 3.0e38f) return CSA2_ERR_INVALID_ARG;
     if (a->batch == 0 || a->n_tokens == 0) return CSA2_OK;

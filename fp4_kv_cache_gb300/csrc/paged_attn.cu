@@ -50,6 +50,7 @@ constexpr float kUnset = 1e30f;         // -maximum of a row that has seen no ke
 // shared memory: Q 9 units | chunks 0..7 | chunk 8, or P^T once S has been computed | the rest
 constexpr int kOffK = 9 * kQUnit, kOffP = kOffK + 8 * kChunk, kOffMisc = kOffP + kChunk;
 
+constexpr uint32_t kNoRow = 0xffffffffu;
 struct TileAt {                          // a key tile, for everyone
     int64_t row0;                        // its row tile: first row in q, rows, place in lo and hi
     int32_t rows, item;
@@ -64,7 +65,7 @@ constexpr uint32_t kTail = 8, kPart = 16;     // the row tile began in a CTA bef
 struct Misc {
     uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
     uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
-    int32_t slot[kRing][kKeys];         // a key's row of the cache; -1: no key
+    uint2 row[kRing][kKeys];            // where a key's row lies: codes / 16 bytes, scales; kNoRow: no key
     TileAt tile[kRing];
     float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
     float red[4][kRows];
@@ -88,7 +89,6 @@ struct PartDesc {        // per CTA: the row tile it starts and does not finish
 struct AttnParams {
     PagedView C;
     int32_t batch, n_tokens, H, d_v, width, window, ratio, chunks, n_pv;
-    int32_t dense;                // pages follow one another
     float log2_scale;
     uint32_t f0, f4;              // see decode
     const uint16_t *q;
@@ -109,6 +109,14 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
                  "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
                  ::"r"(d), "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(acc) : "memory");
+}
+// What other threads have stored, and this one has seen arrive, comes before its MMAs' reads.  The
+// fence stands here and not behind the stores: a staging warp would wait there for its own, about
+// 300 cycles each time.
+__device__ __forceinline__ void staged_fence()
+{
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_after();
 }
 __device__ __forceinline__ bool elect_one()
 {
@@ -393,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // the pair.  A key's four lanes read 64 bytes of its row; so that eight lanes of a store hold
         // eight different columns, the second chunk's blocks start with their upper half.  Warp w
         // takes tasks w, w + 11, .., three a round: a round is one run of instructions with nothing
-        // to wait for inside, one fence at its end (72 tasks with MMAs beside them took 2,770 cycles
-        // with six tasks a round, 3,750 with two).  Chunk 8 makes 16 tasks of half the size, spread so
+        // to wait for inside (72 tasks with MMAs beside them took 2,770 cycles with six tasks a round,
+        // 3,750 with two).  Chunk 8 makes 16 tasks of half the size, spread so
         // that each warp has about the same.  A round's rows of the next tile are on their way as
         // soon as its registers are free; where they lie is read before it starts.
         const int w = warp - kStageWarp, key8 = lane >> 2, q = lane & 3;
@@ -409,21 +417,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         constexpr bool kDeep = FMT == CSA2P_MXFP4 || FMT == CSA2P_NVFP4_E4M3_16;   // registers for a tile ahead
         auto live = [&](int task) { return task < 64 && (FULL || (task >> 4) < pairs); };
         const uint8_t *codes = P.C.codes + lane_code, *scales = P.C.scales + lane_scale;
-        // where a row lies: dense pages follow one another
-        auto code_of = [&](int32_t sl) -> const uint8_t * { return codes + (P.dense ? (int64_t)sl * P.C.code_row : P.C.code_at(sl)); };
-        auto scale_of = [&](int32_t sl) -> const uint8_t * { return scales + (P.dense ? (int64_t)sl * P.C.scale_row : P.C.scale_at(sl)); };
-        auto load_task = [&](Raw<FMT, 4> &r, int32_t sl, int task) {
+        auto load_task = [&](Raw<FMT, 4> &r, uint2 a, int task) {
             const int cp = task >> 4;
-            if (sl >= 0 && live(task) && (FULL || 4 * cp + q < n_blocks))
-                load_raw(r, code_of(sl) + cp * code_bytes<FMT>(128), scale_of(sl) + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
+            if (a.x != kNoRow && live(task) && (FULL || 4 * cp + q < n_blocks))
+                load_raw(r, codes + (uint64_t)a.x * 16 + cp * code_bytes<FMT>(128), scales + a.y + cp * (FMT == CSA2P_NVFP4_E4M3_16 ? 8 : 4));
             else
                 zero_raw(r);
         };
-        auto where = [&](int32_t (&a)[6], int ring) {
+        auto where = [&](uint2 (&a)[6], int ring) {
 #pragma unroll
-            for (int k = 0; k < 6; ++k) a[k] = M.slot[ring][8 * ((w + kStageWarps * k) & 15) + key8];
+            for (int k = 0; k < 6; ++k) a[k] = M.row[ring][8 * ((w + kStageWarps * k) & 15) + key8];
         };
-        auto load_round = [&](Raw<FMT, 4> (&r)[3], const int32_t (&a)[6], int k0) {
+        auto load_round = [&](Raw<FMT, 4> (&r)[3], const uint2 (&a)[6], int k0) {
 #pragma unroll
             for (int k = 0; k < 3; ++k) load_task(r[k], a[k0 + k], w + kStageWarps * (k0 + k));
         };
@@ -433,18 +438,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 if (i >= jn) break;
-                const int32_t sl = M.slot[ring][8 * (j0 + i * jstep) + key8];
-                if (sl >= 0 && (FULL || 16 + (q >> 1) < n_blocks))
-                    load_raw(r8[i], code_of(sl) - lane_code / 2 + code_bytes<FMT>(512),
-                             scale_of(sl) - lane_scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
+                const uint2 a = M.row[ring][8 * (j0 + i * jstep) + key8];
+                if (a.x != kNoRow && (FULL || 16 + (q >> 1) < n_blocks))
+                    load_raw(r8[i], codes + (uint64_t)a.x * 16 - lane_code / 2 + code_bytes<FMT>(512),
+                             scales + a.y - lane_scale + (FMT == CSA2P_NVFP4_E4M3_16 ? 32 + q : 16 + (q >> 1)));
                 else
                     zero_raw(r8[i]);
             }
         };
-        auto store_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n, int k0) {
+        const int c8 = ((2 * q) ^ key8) << 4;
+        auto store_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n, int k0, bool with_tail) {
             // the chunks have been left by the product before: blocks are done in order
-            const int last = min(w + kStageWarps * (k0 + 2), 63);
-            if (n > 0) ok = wait_bar(&M.pv_done[min(min(last >> 4, pairs - 1), n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
+            const int last = with_tail ? 63 : min(w + kStageWarps * (k0 + 2), 63);
+            if (n > 0) ok = wait_bar(&M.pv_done[with_tail ? n_pv - 1 : min(min(last >> 4, pairs - 1), n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
             bool odd[3];
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
@@ -468,12 +474,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                                     1u << (8 * (kg & 3) + key8));
                 }
             }
-            tc::fence_proxy_async_smem();
+            if (with_tail) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (i >= jn) break;
+                    const int kg = j0 + i * jstep;
+                    uint32_t v[8];
+                    decode(r8[i], v, P.f0, P.f4);
+                    uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
+                    *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
+                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
+                }
+            }
             __syncwarp();
             if (lane < 3 && live(w + kStageWarps * (k0 + lane))) tc::mbar_arrive(&M.full_k[(w + kStageWarps * (k0 + lane)) >> 4]);
+            if (with_tail && lane < jn) tc::mbar_arrive(&M.full_k[4]);
         };
         Raw<FMT, 4> ra[3], rb[3];
-        int32_t at[6];
+        uint2 at[6];
         if (units > 0) {
             ok = wait_bar(&M.rows[0], 0, &M.abort);
             if (ok && kDeep) {
@@ -510,36 +529,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (kDeep) {
                 if (tail) load_tail(ring);
                 where(at, ring1);                     // stale where there is no next tile: not used
-                store_round(ra, n, 0);
+                store_round(ra, n, 0, false);
                 if (more) load_round(ra, at, 0);
-                store_round(rb, n, 3);
+                store_round(rb, n, 3, tail);
                 if (more) load_round(rb, at, 3);
             } else {
                 where(at, ring);
                 load_round(ra, at, 0);
-                store_round(ra, n, 0);
+                store_round(ra, n, 0, false);
                 load_round(ra, at, 3);
-                store_round(ra, n, 3);
                 if (tail) load_tail(ring);
-            }
-            if (tail) {
-                if (n > 0) ok = wait_bar(&M.pv_done[n_pv - 1], (n - 1) & 1, &M.abort) && ok;
-                const int c8 = ((2 * q) ^ key8) << 4;
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    if (i >= jn) break;
-                    const int kg = j0 + i * jstep;
-                    uint32_t v[8];
-                    decode(r8[i], v, P.f0, P.f4);
-                    uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
-                    *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
-                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    for (int i = 0; i < jn; ++i) tc::mbar_arrive(&M.full_k[4]);
+                store_round(ra, n, 3, tail);
             }
             ring = ring1;
             round = round1;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if ((c & 1) == 0) {
                     ok = __all_sync(0xffffffffu, wait_bar(&M.full_k[c >> 1], n & 1, &M.abort));
                     if (!ok) break;
-                    tc::tc_fence_after();
+                    staged_fence();
                 }
                 const uint32_t a = k_lo + c * (kChunk / 16), b = q_lo + c * (kQUnit / 16), first = c != 0;
                 if (elect_one()) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             __syncwarp();
             ok = __all_sync(0xffffffffu, wait_bar(&M.full_p, n & 1, &M.abort));
             if (!ok) break;
-            tc::tc_fence_after();
+            staged_fence();
 #pragma unroll 1
             for (int j = 0; j < n_pv; ++j) {
                 const uint32_t a = v_lo + j * (2 * kChunk / 16), d = tmem + 64 + 64 * j;
@@ -611,13 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // rows' bounds.
         auto look = [&]() {
             const int32_t key0 = walk.key0(), k = key0 + key_in;
-            int32_t sl = -1;
+            uint2 at = make_uint2(kNoRow, 0u);
             if (k >= walk.it.lo && k < walk.it.hi) {
                 const int32_t id = P.table[(int64_t)walk.it.b * P.width + (k >> P.C.shift)];
-                if (id >= 0 && id < P.C.n_pages) sl = (int32_t)(((uint32_t)id << P.C.shift) + (k & ((1 << P.C.shift) - 1)));
-                else dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                if (id >= 0 && id < P.C.n_pages) {
+                    const int32_t in = k & ((1 << P.C.shift) - 1);
+                    at.x = (uint32_t)((id * P.C.code_page + (int64_t)in * P.C.code_row) >> 4);
+                    at.y = (uint32_t)(id * P.C.scale_page + (int64_t)in * P.C.scale_row);
+                } else {
+                    dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                }
             }
-            M.slot[ahead_ring][key_in] = sl;
+            M.row[ahead_ring][key_in] = at;
             if (walk.first()) {
                 ++ib;
                 if (key_in < kRows) {                 // rows past the last: as the last
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             failed |= __any_sync(0xffffffffu, !wait_bar(&M.rows[ring], round, &M.abort));
             const TileAt &T = M.tile[ring];
             const uint32_t flags = T.flags;
-            const bool first = flags & kFirst, have = M.slot[ring][key_in] >= 0;
+            const bool first = flags & kFirst, have = M.row[ring][key_in].x != kNoRow;
             if (first) {
                 if (half == 0 && key_in < kRows) {
                     M.m[key_in] = -INFINITY;
@@ -775,7 +780,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4 *>(sm + kOffP + sw128(key_in, 4 * half + i)) = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-                tc::fence_proxy_async_smem();
                 // a logit far above its row's maximum: once more, with the maximum moved
                 if (softmax_any(failed || (!moved && over > kLazy))) {
                     if (moved) { failed = true; break; }
@@ -977,7 +981,6 @@ cudaError_t launch_paged_attn(const csa2p_attn_args &a, const PagedView &v, uint
     P.chunks = (v.d + 63) / 64;
     P.n_pv = (a.d_v + 127) / 128;
     P.log2_scale = a.sm_scale * 1.4426950408889634f;
-    P.dense = v.code_page == (int64_t)v.code_row << v.shift && v.scale_page == (int64_t)v.scale_row << v.shift;
     P.f0 = kCodeAt0;
     P.f4 = kCodeAt4;
     P.q = a.q;

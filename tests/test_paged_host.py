@@ -143,7 +143,8 @@ def attn(**k):
     (dict(batch=-1), INVALID), (dict(batch=paged.MAX_BATCH + 1), INVALID), (dict(n_tokens=-1), INVALID),
     (dict(n_heads=0), INVALID), (dict(n_heads=129), INVALID), (dict(d_v=0), INVALID), (dict(d_v=508), INVALID),
     (dict(d_v=584), INVALID), (dict(d_v=520), UNSUPPORTED), (dict(cache=cache(d=640)), UNSUPPORTED),
-    (dict(width=-1), INVALID), (dict(window=-1), INVALID), (dict(ratio_m=0), INVALID), (dict(sm_scale=0.0), INVALID),
+    (dict(cache=cache(n_pages=1 << 22)), UNSUPPORTED), (dict(cache=cache(code_stride=1 << 33)), UNSUPPORTED),
+    (dict(cache=cache(scale_stride=1 << 29)), UNSUPPORTED), (dict(width=-1), INVALID), (dict(window=-1), INVALID), (dict(ratio_m=0), INVALID), (dict(sm_scale=0.0), INVALID),
     (dict(sm_scale=float("nan")), INVALID), (dict(sm_scale=float("inf")), INVALID), (dict(q=None), INVALID),
     (dict(q=FAKE + 2), INVALID), (dict(block_table=None), INVALID), (dict(lens=None), INVALID), (dict(cu=None), INVALID),
     (dict(pos0=None, ratio_m=2), INVALID), (dict(n_tokens=1 << 25), INVALID)], ids=str)
