@@ -26,6 +26,8 @@
 //
 // Keys past a row tile's bounds, in bad pages or of rows that are not finite are staged as zeros
 // and marked, so that what they hold reaches no query that does not see them.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
@@ -134,6 +136,16 @@ using tc::mbar_wait;
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int32_t *abort)
 {
     return mbar_wait(bar, parity, abort);
+}
+// The same for a warp that stays together: true when every lane has seen the phase.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const int32_t *abort)
+{
+#pragma unroll 1
+    for (uint32_t i = 0; i < tc::kSpinLimit; ++i) {
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+        if ((i & 255u) == 255u && *(const volatile int32_t *)abort) return false;
+    }
+    return false;
 }
 // 256 softmax threads: barrier that tells all of them whether one of them says yes
 __device__ __forceinline__ bool softmax_any(bool v)
@@ -447,49 +459,68 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             }
         };
         const int c8 = ((2 * q) ^ key8) << 4;
-        auto store_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n, int k0, bool with_tail) {
-            // the chunks have been left by the product before: blocks are done in order
-            const int last = with_tail ? 63 : min(w + kStageWarps * (k0 + 2), 63);
-            if (n > 0) ok = wait_bar(&M.pv_done[with_tail ? n_pv - 1 : min(min(last >> 4, pairs - 1), n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
-            bool odd[3];
+        // A block of the product before has left chunks 2 j, 2 j + 1; blocks are done in order.
+        auto left = [&](uint32_t n, int j) {
+            if (n > 0) ok = wait_bar(&M.pv_done[min(j, n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
+        };
+        // tasks w + 11 k for k = k0 .. k0 + K - 1
+        auto store_tasks = [&](Raw<FMT, 4> *r, auto count, uint32_t n, int k0) {
+            constexpr int K = decltype(count)::value;
+            bool odd[K], any = false;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
+            for (int k = 0; k < K; ++k) {
                 const int task = w + kStageWarps * (k0 + k);
                 uint32_t v[16];
                 swap_raw(r[k], swap);
                 decode(r[k], v, P.f0, P.f4);
                 odd[k] = unusual(r[k]) && live(task);
+                any |= odd[k];
                 uint8_t *u = sm + place + (task >> 4) * 2 * kChunk + (task & 15) * 1024;
                 if (live(task))
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         *reinterpret_cast<uint4 *>(u + col[i]) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
-            if (odd[0] || odd[1] || odd[2]) {
+            if (any) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
+                for (int k = 0; k < K; ++k) {
                     const int task = w + kStageWarps * (k0 + k), kg = task & 15;
                     if (odd[k])
                         decode_slow(r[k], sm + place + (task >> 4) * 2 * kChunk + kg * 1024, col[0], 16, &M.nan[n & 1][kg >> 2],
                                     1u << (8 * (kg & 3) + key8));
                 }
             }
-            if (with_tail) {
+            __syncwarp();
+            if (lane < K && live(w + kStageWarps * (k0 + lane))) tc::mbar_arrive(&M.full_k[(w + kStageWarps * (k0 + lane)) >> 4]);
+        };
+        auto store_tail = [&](uint32_t n) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    if (i >= jn) break;
-                    const int kg = j0 + i * jstep;
-                    uint32_t v[8];
-                    decode(r8[i], v, P.f0, P.f4);
-                    uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
-                    *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
-                    if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
-                }
+            for (int i = 0; i < 3; ++i) {
+                if (i >= jn) break;
+                const int kg = j0 + i * jstep;
+                uint32_t v[8];
+                decode(r8[i], v, P.f0, P.f4);
+                uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
+                *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
+                if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
             }
             __syncwarp();
-            if (lane < 3 && live(w + kStageWarps * (k0 + lane))) tc::mbar_arrive(&M.full_k[(w + kStageWarps * (k0 + lane)) >> 4]);
-            if (with_tail && lane < jn) tc::mbar_arrive(&M.full_k[4]);
+            if (lane < jn) tc::mbar_arrive(&M.full_k[4]);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        auto first_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n) {
+            left(n, 0);
+            store_tasks(r, One{}, n, 0);
+            left(n, min((w + 2 * kStageWarps) >> 4, pairs - 1));
+            store_tasks(r + 1, Two{}, n, 1);
+        };
+        auto second_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n) {
+            left(n, 3);
+            store_tasks(r, Two{}, n, 3);
+            store_tasks(r + 2, One{}, n, 5);
+            if (tail) store_tail(n);
         };
         Raw<FMT, 4> ra[3], rb[3];
         uint2 at[6];
@@ -529,17 +560,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (kDeep) {
                 if (tail) load_tail(ring);
                 where(at, ring1);                     // stale where there is no next tile: not used
-                store_round(ra, n, 0, false);
+                first_round(ra, n);
                 if (more) load_round(ra, at, 0);
-                store_round(rb, n, 3, tail);
+                second_round(rb, n);
                 if (more) load_round(rb, at, 3);
             } else {
                 where(at, ring);
                 load_round(ra, at, 0);
-                store_round(ra, n, 0, false);
+                first_round(ra, n);
                 load_round(ra, at, 3);
                 if (tail) load_tail(ring);
-                store_round(ra, n, 3, tail);
+                second_round(ra, n);
             }
             ring = ring1;
             round = round1;
@@ -556,48 +587,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint32_t upper = (uint32_t)(dk >> 32);      // stride, version, swizzle: the same for all
         const uint32_t k_lo = (uint32_t)dk, v_lo = (uint32_t)dv, q_lo = (uint32_t)tc::smem_desc(base, 16, 1024, tc::kSwizzle128B);
         const uint32_t p_lo = (uint32_t)tc::smem_desc(base + kOffP, kChunk, 1024, tc::kSwizzle128B);
+        const bool leader = elect_one();
         bool ok = true;
         int ring = 0;
 #pragma unroll 1
         for (uint32_t n = 0; n < (uint32_t)units; ++n) {
+            // a pair of chunks as soon as it is staged; nothing but the MMAs between two waits
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                if ((c & 1) == 0) {
-                    ok = __all_sync(0xffffffffu, wait_bar(&M.full_k[c >> 1], n & 1, &M.abort));
-                    if (!ok) break;
-                    staged_fence();
+            for (int g = 0; 2 * g < chunks; ++g) {
+                ok = wait_warp(&M.full_k[g], n & 1, &M.abort);
+                if (!ok) break;
+                staged_fence();
+                if (leader) {
+                    for (int c = 2 * g; c < min(2 * g + 2, chunks); ++c) {
+                        const uint32_t a = k_lo + c * (kChunk / 16), b = q_lo + c * (kQUnit / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma(tmem, a + k * 2, b + k * 2, upper, instr(0, 0), c + k != 0);
+                    }
                 }
-                const uint32_t a = k_lo + c * (kChunk / 16), b = q_lo + c * (kQUnit / 16), first = c != 0;
-                if (elect_one()) {
-                    mma(tmem, a, b, upper, instr(0, 0), first);
-                    mma(tmem, a + 2, b + 2, upper, instr(0, 0), 1);
-                    mma(tmem, a + 4, b + 4, upper, instr(0, 0), 1);
-                    mma(tmem, a + 6, b + 6, upper, instr(0, 0), 1);
-                }
-                __syncwarp();
             }
             if (!ok) break;
             const uint32_t later = (M.tile[ring].flags & kFirst) == 0;   // read before the softmax may go on
             ring = ring == kRing - 1 ? 0 : ring + 1;
-            if (elect_one()) tc::tc_commit(&M.s_done);
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, wait_bar(&M.full_p, n & 1, &M.abort));
+            if (leader) tc::tc_commit(&M.s_done);
+            ok = wait_warp(&M.full_p, n & 1, &M.abort);
             if (!ok) break;
             staged_fence();
-#pragma unroll 1
-            for (int j = 0; j < n_pv; ++j) {
-                const uint32_t a = v_lo + j * (2 * kChunk / 16), d = tmem + 64 + 64 * j;
-                if (elect_one()) {
-                    mma(d, a, p_lo, upper, instr(1, 1), later);
+            if (leader) {
 #pragma unroll
-                    for (int k = 1; k < 8; ++k) mma(d, a + k * 128, p_lo + k * 128, upper, instr(1, 1), 1);
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= n_pv) break;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma(tmem + 64 + 64 * j, v_lo + j * (2 * kChunk / 16) + k * 128, p_lo + k * 128, upper, instr(1, 1), k ? 1 : later);
                     tc::tc_commit(&M.pv_done[j]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
         if (!ok) M.abort = 1;
-        if (elect_one()) tc::tc_commit(&M.drained);       // nothing may still run when the CTA leaves
+        __syncwarp();
+        if (leader) tc::tc_commit(&M.drained);        // nothing may still run when the CTA leaves
         __syncwarp();
     } else {
         // ============================================================ softmax and output
@@ -786,15 +816,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     moved = true;
                     continue;
                 }
+                tc::tc_fence_before();
+                if (tid < 4) M.nan[ph][tid] = 0;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&M.full_p);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) l[c] += __uint_as_float(r[c]);
                 break;
             }
             if (failed) break;
-            tc::tc_fence_before();
-            if (tid < 4) M.nan[ph][tid] = 0;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&M.full_p);
             if (flags & kLast) {
                 // ---- output, or a part of it: sums over the keys, then a lane has one dim of every row
                 const int rows = T.rows;
