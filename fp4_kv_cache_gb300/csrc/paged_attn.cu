@@ -64,24 +64,6 @@ constexpr uint32_t kFirst = 1, kLast = 2;     // of this CTA's key tiles of the 
 constexpr uint32_t kEdge = 4;                 // some row does not see every key
 constexpr uint32_t kTail = 8, kPart = 16;     // the row tile began in a CTA before; others have parts of it
 
-struct Misc {
-    uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
-    uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
-    uint2 row[kRing][kKeys];            // where a key's row lies: codes / 16 bytes, scales; kNoRow: no key
-    TileAt tile[kRing];
-    float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
-    float red[4][kRows];
-    int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile
-    int64_t scan[kThreads / 32];
-    int64_t item_unit;                  // first unit of this CTA's first item
-    uint32_t nan[2][4];                 // keys with a value that is not finite
-    int32_t b, j, off;
-    uint32_t tmem;
-    int32_t abort;
-};
-constexpr int kSmem = kOffMisc + (int)sizeof(Misc);
-static_assert(kSmem <= 232448, "does not fit the shared memory of a CTA");
-
 struct PartDesc {        // per CTA: the row tile it starts and does not finish
     int32_t parts;       // 0: none
     int32_t rows;
@@ -262,12 +244,12 @@ struct Walk {
         left -= n;
         at = 0;
     }
-    __device__ __forceinline__ bool begin(const AttnParams &P, const Misc &M, int64_t units)
+    __device__ __forceinline__ bool begin(const AttnParams &P, int32_t b, int32_t j, int32_t first, int64_t units)
     {
         left = units;
         if (units <= 0) return false;
-        it = load_item(P, M.b, M.j);
-        off = M.off;
+        it = load_item(P, b, j);
+        off = first;
         take();
         return true;
     }
@@ -290,6 +272,25 @@ struct Walk {
     __device__ __forceinline__ bool last() const { return at == n - 1; }
     __device__ __forceinline__ int32_t key0() const { return (it.k0 + off + at) * kKeys; }
 };
+
+struct Misc {
+    uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
+    uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
+    uint2 row[kRing][kKeys];            // where a key's row lies: codes / 16 bytes, scales; kNoRow: no key
+    TileAt tile[kRing];
+    float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
+    float red[4][kRows];
+    int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile
+    int64_t scan[kThreads / 32];
+    int64_t item_unit;                  // first unit of this CTA's first item
+    Walk walk[4];                       // of the upper half's warps: two tiles ahead
+    uint32_t nan[2][4];                 // keys with a value that is not finite
+    int32_t b, j, off;
+    uint32_t tmem;
+    int32_t abort;
+};
+constexpr int kSmem = kOffMisc + (int)sizeof(Misc);
+static_assert(kSmem <= 232448, "does not fit the shared memory of a CTA");
 
 // Block-wide exclusive sum over the threads.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *buf, int64_t &total)
@@ -436,13 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             else
                 zero_raw(r);
         };
-        auto where = [&](uint2 (&a)[6], int ring) {
+        auto load_round = [&](Raw<FMT, 4> (&r)[3], int ring, int k0) {
+            uint2 a[3];
 #pragma unroll
-            for (int k = 0; k < 6; ++k) a[k] = M.row[ring][8 * ((w + kStageWarps * k) & 15) + key8];
-        };
-        auto load_round = [&](Raw<FMT, 4> (&r)[3], const uint2 (&a)[6], int k0) {
+            for (int k = 0; k < 3; ++k) a[k] = M.row[ring][8 * ((w + kStageWarps * (k0 + k)) & 15) + key8];
 #pragma unroll
-            for (int k = 0; k < 3; ++k) load_task(r[k], a[k0 + k], w + kStageWarps * (k0 + k));
+            for (int k = 0; k < 3; ++k) load_task(r[k], a[k], w + kStageWarps * (k0 + k));
         };
         Raw<FMT, 2> r8[3];                            // chunk 8
         auto load_tail = [&](int ring) {
@@ -523,13 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (tail) store_tail(n);
         };
         Raw<FMT, 4> ra[3], rb[3];
-        uint2 at[6];
         if (units > 0) {
             ok = wait_bar(&M.rows[0], 0, &M.abort);
             if (ok && kDeep) {
-                where(at, 0);
-                load_round(ra, at, 0);
-                load_round(rb, at, 3);
+                load_round(ra, 0, 0);
+                load_round(rb, 0, 3);
             }
         }
         int ring = 0;                                 // n mod kRing, and the parity of the ring's round
@@ -559,16 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
             if (kDeep) {
                 if (tail) load_tail(ring);
-                where(at, ring1);                     // stale where there is no next tile: not used
                 first_round(ra, n);
-                if (more) load_round(ra, at, 0);
+                if (more) load_round(ra, ring1, 0);
                 second_round(rb, n);
-                if (more) load_round(rb, at, 3);
+                if (more) load_round(rb, ring1, 3);
             } else {
-                where(at, ring);
-                load_round(ra, at, 0);
+                load_round(ra, ring, 0);
                 first_round(ra, n);
-                load_round(ra, at, 3);
+                load_round(ra, ring, 3);
                 if (tail) load_tail(ring);
                 second_round(ra, n);
             }
@@ -634,7 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // Thread (key, half): the key of its tensor memory lane, rows 32 half .. 32 half + 31.
         const int quad = warp & 3, half = warp >> 2, key_in = 32 * quad + lane, c_lo = 32 * half;
         const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16) + c_lo;
-        Walk walk;                                    // of the upper half's threads: two tiles ahead
+        // The walk lies in shared memory, a copy for each warp that goes it: its 22 words would not
+        // fit beside the logits (windows of 128 rows over an MXFP8 cache: 350 -> 326 us).
+        Walk &walk = M.walk[quad];
         bool failed = false;
         int ahead_ring = 0, ib = -1;
         // What a tile needs, for everyone: where its keys' rows lie, and at a row tile's start the
@@ -682,15 +680,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             ahead_ring = ahead_ring == kRing - 1 ? 0 : ahead_ring + 1;
         };
         bool more = false;                            // the walk has a tile that is not looked up yet
+        auto go_on = [&]() {                          // after look
+            __syncwarp();
+            bool on = false;
+            if (lane == 0) on = walk.next(P);
+            more = __any_sync(0xffffffffu, on);
+        };
         if (half == 1) {
-            more = walk.begin(P, M, units);
+            if (lane == 0) more = walk.begin(P, M.b, M.j, M.off, units);
+            more = __any_sync(0xffffffffu, more);
             if (more) {
                 look();
-                more = walk.next(P);
+                go_on();
             }
             if (more) {
                 look();
-                more = walk.next(P);
+                go_on();
             }
         }
         float l[32];                                  // sums of weights: this thread's key in each tile
@@ -716,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 // a tile looked up two ahead takes the place of the one before this one, whose staging
                 // and softmax are done
                 look();
-                more = walk.next(P);
+                go_on();
             }
             failed |= __any_sync(0xffffffffu, !wait_bar(&M.full_k[tail ? 4 : pairs - 1], ph, &M.abort));
             const bool nan = (M.nan[ph][quad] >> lane) & 1u;
