@@ -129,6 +129,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const 
     }
     return false;
 }
+// n bytes on their way to the L2 cache; address and n are multiples of 16
+__device__ __forceinline__ void prefetch_l2(const void *p, int n)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+}
 // 256 softmax threads: barrier that tells all of them whether one of them says yes
 __device__ __forceinline__ bool softmax_any(bool v)
 {
@@ -278,9 +283,9 @@ struct Misc {
     uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
     uint2 row[kRing][kKeys];            // where a key's row lies: codes / 16 bytes, scales; kNoRow: no key
     TileAt tile[kRing];
-    float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
+    alignas(16) float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
     float red[4][kRows];
-    int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile
+    alignas(16) int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile
     int64_t scan[kThreads / 32];
     int64_t item_unit;                  // first unit of this CTA's first item
     Walk walk[4];                       // of the upper half's warps: two tiles ahead
@@ -544,14 +549,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int pieces = FULL ? 72 : P.C.d / 8, all = chunks * 8, rows = M.tile[ring].rows;
                 const uint16_t *src = P.q + M.tile[ring].row0 * P.C.d;
-#pragma unroll 4
+                int r = (tid - 32 * kStageWarp) / 72, p = (tid - 32 * kStageWarp) % 72;
+#pragma unroll 7
                 for (int e = tid - 32 * kStageWarp; e < 64 * 72; e += kStageThreads) {
-                    const int r = e / 72, p = e - 72 * r;
-                    if (!FULL && p >= all) continue;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows && (FULL || p < pieces)) v = *reinterpret_cast<const uint4 *>(src + r * P.C.d + 8 * p);
-                    *reinterpret_cast<uint4 *>(sm + (p >> 3) * kQUnit + sw128(r, p & 7)) =
-                        make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u), prmt(v.y, v.w, 0x7632u));
+                    if (FULL || p < all) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < rows && (FULL || p < pieces)) v = *reinterpret_cast<const uint4 *>(src + (FULL ? 8 * e : r * P.C.d + 8 * p));
+                        *reinterpret_cast<uint4 *>(sm + (p >> 3) * kQUnit + sw128(r, p & 7)) =
+                            make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u), prmt(v.y, v.w, 0x7632u));
+                    }
+                    p += kStageThreads % 72;
+                    r += kStageThreads / 72;
+                    if (p >= 72) {
+                        p -= 72;
+                        ++r;
+                    }
                 }
             }
             if (more) ok = wait_bar(&M.rows[ring1], round1, &M.abort) && ok;
@@ -661,7 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     M.lo[ib & 3][key_in] = lo;
                     M.hi[ib & 3][key_in] = hi;
                 }
-                if (key_in == 0 && walk.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                if (key_in == 0) {
+                    if (walk.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                    prefetch_l2(P.q + walk.it.row0 * P.C.d, walk.it.rows * P.C.d * 2);
+                }
             }
             if (key_in == 0) {
                 TileAt t;
@@ -737,9 +752,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     tc::tc_ld_32x32b_x16(lane_t + c0, r);
                     tc::tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const bool see = have && key >= M.lo[item][c_lo + c0 + c] && key < M.hi[item][c_lo + c0 + c];
-                        r[c] = !see ? 0xff800000u : nan ? 0x7fc00000u : r[c];
+                    for (int c = 0; c < 16; c += 4) {
+                        const int4 lo = *reinterpret_cast<const int4 *>(&M.lo[item][c_lo + c0 + c]);
+                        const int4 hi = *reinterpret_cast<const int4 *>(&M.hi[item][c_lo + c0 + c]);
+                        auto seen = [&](uint32_t x, int l, int h) { return !(have && key >= l && key < h) ? 0xff800000u : nan ? 0x7fc00000u : x; };
+                        r[c] = seen(r[c], lo.x, hi.x);
+                        r[c + 1] = seen(r[c + 1], lo.y, hi.y);
+                        r[c + 2] = seen(r[c + 2], lo.z, hi.z);
+                        r[c + 3] = seen(r[c + 3], lo.w, hi.w);
                     }
                     tc::tc_st_32x32b_x16(lane_t + c0, r);
                 }
@@ -866,34 +886,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                 }
                 softmax_any(false);
-                // the dim that this lane's place stands for, and of the pair that it writes
-                const int dim_in = (key_in & ~7) | ((key_in & 1) << 2) | ((key_in & 7) >> 1);
-                const bool odd = (lane & 2) != 0;
+                // A lane has one dim of 16 rows.  Parts are stored like that, in the dims' order; an output
+                // is packed in pairs of rows and turned over between the eight lanes of a 16-byte piece.
+                const int dim_in = (key_in & ~7) | ((key_in & 1) << 2) | ((key_in & 7) >> 1), t = lane & 7;
 #pragma unroll 1
-                for (int j = 0; j < n_pv; ++j)
-#pragma unroll 1
-                    for (int c0 = 0; c0 < 32; c0 += 16) {
-                        const int r0 = c_lo + c0, dim = 128 * j + dim_in;
-                        if (r0 >= rows) break;
-                        uint32_t o[16];
-                        tc::tc_ld_32x32b_x16(lane_t + 64 + 64 * j + c0, o);
-                        tc::tc_wait_ld();
-                        if (part) {
-                            if (dim < P.d_v)
+                for (int i = 0; i < 2 * n_pv; ++i) {
+                    const int r0 = c_lo + 16 * (i & 1), dim0 = 128 * (i >> 1);
+                    if (r0 >= rows) continue;
+                    uint32_t o[16], v[8];
+                    tc::tc_ld_32x32b_x16(lane_t + 64 + 64 * (i >> 1) + 16 * (i & 1), o);
+                    tc::tc_wait_ld();
+                    if (part) {
+                        float *to = P.part_o + (slot + r0) * P.d_v + dim0 + dim_in;
+                        if (dim0 + dim_in < P.d_v)
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) P.part_o[(slot + r0 + c) * P.d_v + dim] = __uint_as_float(o[c]);
-                        } else {
+                            for (int c = 0; c < 16; ++c) to[(int64_t)c * P.d_v] = __uint_as_float(o[c]);
+                        continue;
+                    }
 #pragma unroll
-                            for (int c = 0; c < 16; c += 2) {     // lanes two apart hold neighbouring dims
-                                const float x = __uint_as_float(o[c]) * M.fac[r0 + c], y = __uint_as_float(o[c + 1]) * M.fac[r0 + c + 1];
-                                const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 2);
-                                const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(other, y) : __floats2bfloat162_rn(x, other);
-                                const int r = r0 + c + (odd ? 1 : 0);
-                                if (r < rows && dim < P.d_v)
-                                    *reinterpret_cast<__nv_bfloat162 *>(P.out + (row0 + r) * P.d_v + (dim & ~1)) = b;
-                            }
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&M.fac[r0 + c]);
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[c]) * f.x, __uint_as_float(o[c + 1]) * f.y);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[c + 2]) * f.z, __uint_as_float(o[c + 3]) * f.w);
+                        v[c / 2] = *reinterpret_cast<const uint32_t *>(&x);
+                        v[c / 2 + 1] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+#pragma unroll
+                    for (int st = 4; st; st >>= 1) {
+                        const bool up = (lane & st) != 0;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (k & st) continue;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k | st], st);
+                            if (up) v[k] = got;
+                            else v[k | st] = got;
                         }
                     }
+                    // v[k]: rows r0 + 2 t, r0 + 2 t + 1 of the dim that place k stands for
+                    uint16_t *to = P.out + (row0 + r0 + 2 * t) * P.d_v + dim0 + (key_in & ~7);
+                    if (dim0 + (key_in & ~7) < P.d_v) {
+                        if (r0 + 2 * t < rows)
+                            *reinterpret_cast<uint4 *>(to) =
+                                make_uint4(prmt(v[0], v[2], 0x5410u), prmt(v[4], v[6], 0x5410u), prmt(v[1], v[3], 0x5410u), prmt(v[5], v[7], 0x5410u));
+                        if (r0 + 2 * t + 1 < rows)
+                            *reinterpret_cast<uint4 *>(to + P.d_v) =
+                                make_uint4(prmt(v[0], v[2], 0x7632u), prmt(v[4], v[6], 0x7632u), prmt(v[1], v[3], 0x7632u), prmt(v[5], v[7], 0x7632u));
+                    }
+                }
                 tc::tc_fence_before();
                 unit += nt;
             }
