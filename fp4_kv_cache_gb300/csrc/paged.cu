@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(1024) paged_read_kernel(const PagedView C, con
         for (int k = 0; k < U; ++k) {
             if (sls[k] < 0) continue;
             uint16_t *to = out + (r0 + k * blockDim.y + threadIdx.y) * ldo + 16 * part;
-            if (FMT != CSA2P_BF16 && unusual(raw[k])) {
+            if (FMT != CSA2P_BF16 && special(raw[k])) {
                 read_slow(raw[k], to);
                 continue;
             }

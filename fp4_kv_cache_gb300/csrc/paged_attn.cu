@@ -134,6 +134,13 @@ __device__ __forceinline__ void prefetch_l2(const void *p, int n)
 {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
+// the warp's largest; NaN counts only where there is nothing else
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 256 softmax threads: barrier that tells all of them whether one of them says yes
 __device__ __forceinline__ bool softmax_any(bool v)
 {
@@ -469,6 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         auto left = [&](uint32_t n, int j) {
             if (n > 0) ok = wait_bar(&M.pv_done[min(j, n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
         };
+        // Special channels of key group kg, as stored; a key that is not finite is marked.
+        auto rest = [&](const auto &r, uint8_t *u, int col0, uint32_t n, int kg) {
+            if (mend(r, u, col0)) atomicOr(&M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
+        };
         // tasks w + 11 k for k = k0 .. k0 + K - 1
         auto store_tasks = [&](Raw<FMT, 4> *r, auto count, uint32_t n, int k0) {
             constexpr int K = decltype(count)::value;
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 uint32_t v[16];
                 swap_raw(r[k], swap);
                 decode(r[k], v, P.f0, P.f4);
-                odd[k] = unusual(r[k]) && live(task);
+                odd[k] = special(r[k]) && live(task);
                 any |= odd[k];
                 uint8_t *u = sm + place + (task >> 4) * 2 * kChunk + (task & 15) * 1024;
                 if (live(task))
@@ -490,10 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (any) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const int task = w + kStageWarps * (k0 + k), kg = task & 15;
-                    if (odd[k])
-                        decode_slow(r[k], sm + place + (task >> 4) * 2 * kChunk + kg * 1024, col[0], 16, &M.nan[n & 1][kg >> 2],
-                                    1u << (8 * (kg & 3) + key8));
+                    const int task = w + kStageWarps * (k0 + k);
+                    if (odd[k]) rest(r[k], sm + place + (task >> 4) * 2 * kChunk + (task & 15) * 1024, col[0], n, task & 15);
                 }
             }
             __syncwarp();
@@ -509,7 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 uint8_t *u = sm + kOffP + kg * 1024 + key8 * 128;
                 *reinterpret_cast<uint4 *>(u + c8) = make_uint4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<uint4 *>(u + (c8 ^ 16)) = make_uint4(v[4], v[5], v[6], v[7]);
-                if (unusual(r8[i])) decode_slow(r8[i], u, c8, 16, &M.nan[n & 1][kg >> 2], 1u << (8 * (kg & 3) + key8));
+            }
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) any |= i < jn && special(r8[i]);
+            if (any) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int kg = j0 + i * jstep;
+                    if (i < jn && special(r8[i])) rest(r8[i], sm + kOffP + kg * 1024 + key8 * 128, c8, n, kg);
+                }
             }
             __syncwarp();
             if (lane < jn) tc::mbar_arrive(&M.full_k[4]);
@@ -551,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const int pieces = FULL ? 72 : P.C.d / 8, all = chunks * 8, rows = M.tile[ring].rows;
                 const uint16_t *src = P.q + M.tile[ring].row0 * P.C.d;
                 int r = (tid - 32 * kStageWarp) / 72, p = (tid - 32 * kStageWarp) % 72;
-#pragma unroll 7
+#pragma unroll 4
                 for (int e = tid - 32 * kStageWarp; e < 64 * 72; e += kStageThreads) {
                     if (FULL || p < all) {
                         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -773,19 +791,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if (moved) {
                     // ---- new maxima, reduced over the keys
                     if (softmax_any(failed)) { failed = true; break; }
-#pragma unroll 1
-                    for (int c0 = 0; c0 < 32; c0 += 16) {
-                        uint32_t r[16];
-                        float v[16];
-                        tc::tc_ld_32x32b_x16(lane_t + c0, r);
+                    {
+                        uint32_t r[32];
+                        tc::tc_ld_32x32b_x32(lane_t, r);
                         tc::tc_wait_ld();
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float x = __uint_as_float(r[c]);
-                            v[c] = x != x ? -INFINITY : x * P.log2_scale;
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = warp_max(__uint_as_float(r[c]) * P.log2_scale);
+                            top = lane == c ? x : top;
                         }
-                        const float top = warp_reduce16<true>(v, lane);
-                        if ((lane & 1) == 0) M.red[quad][c_lo + c0 + (lane >> 1)] = top;
+                        M.red[quad][c_lo + lane] = top;
                     }
                     softmax_any(false);
                     if (tid < kRows) {

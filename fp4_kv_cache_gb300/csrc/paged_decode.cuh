@@ -93,10 +93,9 @@ __device__ __forceinline__ void swap_raw(Raw<FMT, N> &r, bool swap)
     if (FMT == CSA2P_NVFP4_E4M3_16 && N == 4) r.sb = swap ? prmt(r.sb, 0u, 0x4401u) : r.sb;
 }
 
-// Whether these channels need decode_slow: scales that one product cannot apply, and what is not
-// finite.
+// Whether decode is not enough: something is not finite, or one factor cannot hold the scale.
 template <int FMT, int N>
-__device__ __forceinline__ bool unusual(const Raw<FMT, N> &r)
+__device__ __forceinline__ bool special(const Raw<FMT, N> &r)
 {
     constexpr int kW = Raw<FMT, N>::kWords;
     uint32_t e = 0;
@@ -114,7 +113,7 @@ __device__ __forceinline__ bool unusual(const Raw<FMT, N> &r)
     return r.sb > 128u;
 }
 
-// N 16-byte pieces (eight channels each, in the order 0 4 1 5 2 6 3 7) of bf16, nothing unusual
+// N 16-byte pieces (eight channels each, in the order 0 4 1 5 2 6 3 7) of bf16, nothing special
 // among them.
 //
 // 4-bit codes: n = two codes, one in the low bits of each half of a word; n x (2^12 + 2^6) has the
@@ -136,7 +135,7 @@ __device__ __forceinline__ void decode(const Raw<FMT, N> &r, uint32_t (&v)[4 * N
             }
     } else if (FMT == CSA2P_MXFP8) {
         // code bits as bf16 bits: value x 2^-120; x 2^(120 + sb - 127)
-        const __nv_bfloat162 m = bf2((r.sb + 120u) << 7);
+        const __nv_bfloat162 m = bf2((min(r.sb, 134u) + 120u) << 7);
 #pragma unroll
         for (int h = 0; h < N; ++h)
 #pragma unroll
@@ -147,7 +146,7 @@ __device__ __forceinline__ void decode(const Raw<FMT, N> &r, uint32_t (&v)[4 * N
     } else {
         constexpr bool nv = FMT == CSA2P_NVFP4_E4M3_16;
         // E8M0: x 2^(126 + sb - 127); E4M3: x 2^126, then the scale (both products exact)
-        const uint32_t mb = nv ? 253u * 0x00800080u : (r.sb + 126u) * 0x00800080u;
+        const uint32_t mb = nv ? 253u * 0x00800080u : (min(r.sb, 128u) + 126u) * 0x00800080u;
         const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&mb);
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -169,48 +168,30 @@ __device__ __forceinline__ void decode(const Raw<FMT, N> &r, uint32_t (&v)[4 * N
     }
 }
 
-// The same for anything, written over what decode left: each value is code x scale in float32
-// (exact), rounded to bf16 once.  If a value or a scale is not finite all are zero and the key's
-// bit is set in *nan.  Scale bytes that could take a value past float32 (no quantised row has
-// them) count as not finite.  Rare, and kept out of the loops' code.
+// Mends what decode made of special channels, where it has been stored (piece i at column
+// col0 ^ 16 i): the rest of the scale in a second product.  Channels that are not finite become
+// zeros, and the answer is true; scale bytes that could take a value past float32 (no quantised row
+// has them) count as not finite.
 template <int FMT, int N>
-__device__ __noinline__ void decode_slow(Raw<FMT, N> r, uint8_t *u, int col0, int col_step, uint32_t *nan, uint32_t bit)
+__device__ __forceinline__ bool mend(const Raw<FMT, N> &r, uint8_t *u, int col0)
 {
-    uint32_t v[4 * N];
-    bool bad = false;
-#pragma unroll 1
-    for (int e = 0; e < 8 * N; ++e) {
-        float x;
-        uint32_t sb = r.sb;
-        if (FMT == CSA2P_BF16) {
-            x = __uint_as_float((r.w[e >> 1] >> (16 * (e & 1))) << 16);
-            bad |= !isfinite(x);
-        } else if (FMT == CSA2P_MXFP8) {
-            x = e4m3_value((r.w[e >> 2] >> (8 * (e & 3))) & 0xffu);
-            bad |= x != x || sb >= 247u;
-            x *= e8m0_value(min(sb, 254u));
-        } else {
-            const uint32_t c = (r.w[e >> 3] >> (4 * (e & 7))) & 15u;
-            x = c & 8u ? -e2m1_mag(c & 7u) : e2m1_mag(c & 7u);
-            if (FMT == CSA2P_NVFP4_E4M3_16) {
-                x *= e4m3_value((sb >> (8 * (e >> 4))) & 0xffu);
-                bad |= x != x;
-            } else {
-                bad |= sb >= 253u;
-                x *= e8m0_value(min(sb, 254u));
-            }
-        }
-        const int at = 2 * (e & 3) + ((e & 7) >> 2);          // place of channel e within its eight
-        const __nv_bfloat16 b = __float2bfloat16_rn(x);
-        const uint32_t h = (uint32_t)__bfloat16_as_ushort(b) << (16 * (at & 1));
-        uint32_t &d = v[4 * (e >> 3) + (at >> 1)];
-        d = (at & 1) ? d | h : h;
+    constexpr uint32_t held = FMT == CSA2P_MXFP8 ? 134u : 128u, most = FMT == CSA2P_MXFP8 ? 246u : 252u;
+    bool bad = true;
+    if (FMT == CSA2P_MXFP4) bad = r.sb > most;
+    if (FMT == CSA2P_MXFP8) {
+        uint32_t e = 0;
+#pragma unroll
+        for (int i = 0; i < Raw<FMT, N>::kWords; ++i) e |= (r.w[i] & 0x7f7f7f7fu) + 0x01010101u;
+        bad = (e & 0x80808080u) != 0 || r.sb > most;
     }
-    if (bad) atomicOr(nan, bit);
+    const __nv_bfloat162 rest = bf2((max(r.sb, held) - held + 127u) << 7);
 #pragma unroll 1
-    for (int i = 0; i < N; ++i)                               // piece i at column col0 ^ (i x col_step)
-        *reinterpret_cast<uint4 *>(u + (col0 ^ (i * col_step))) =
-            bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < N; ++i) {
+        uint4 *p = reinterpret_cast<uint4 *>(u + (col0 ^ (16 * i)));
+        const uint4 v = *p;
+        *p = bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(mul2(v.x, rest), mul2(v.y, rest), mul2(v.z, rest), mul2(v.w, rest));
+    }
+    return bad;
 }
 
 } // namespace csa2
