@@ -719,10 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             __syncwarp();
             bool on = false;
             if (lane == 0) on = walk.next(P);
+            __syncwarp();
             more = __any_sync(0xffffffffu, on);
         };
         if (half == 1) {
             if (lane == 0) more = walk.begin(P, M.b, M.j, M.off, units);
+            __syncwarp();
             more = __any_sync(0xffffffffu, more);
             if (more) {
                 look();

@@ -462,6 +462,20 @@ def test_attn_scales_of_rows(fmt, scale):
     check(AttnCase([200], [4], 16, 128, 128, fmt, 32, q_scale=1.0 / scale, kv_scale=scale, seed=6))
 
 
+@pytest.mark.parametrize("fmt,scale", [(paged.MXFP4, 4.0), (paged.MXFP8, 2.0 ** 14)])
+def test_attn_scales_around_one_factor(fmt, scale):
+    # block scales on both sides of the largest that one bf16 factor holds
+    case = AttnCase([400], [4], 16, 576, 512, fmt, 32, q_scale=1.0 / scale, kv_scale=scale, seed=16)
+    held = 128 if fmt == paged.MXFP4 else 134
+    assert bool((case.cache.scales <= held).any()) and bool((case.cache.scales > held).any())
+    check(case)
+
+
+@pytest.mark.parametrize("window", [127, 128, 129, 255, 256, 257])
+def test_attn_windows_around_tiles(window):
+    check(AttnCase([1000, 130, 257], [5, 130, 1], 64, 576, 512, paged.MXFP8, 128, window=window, seed=window))
+
+
 def test_attn_bad_pages():
     c = AttnCase([300, 400, 200], [4, 2, 3], 64, 576, 512, paged.MXFP4, 16, seed=7)
     c.table[0, 3], c.table[0, 18], c.table[1, 0], c.table[2, 1:] = -1, 2**31 - 1, c.cache.n_pages, -2**31
