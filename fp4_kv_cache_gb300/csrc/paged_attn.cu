@@ -26,6 +26,22 @@
 //
 // Keys past a row tile's bounds, in bad pages or of rows that are not finite are staged as zeros
 // and marked, so that what they hold reaches no query that does not see them.
+//
+// What bounds it.  A tile's two products are 68 MMAs of 128 x 64 x 16, 48 cycles each (the operands'
+// way out of shared memory: 4 + 2 KB at 128 bytes a cycle), 3,264 cycles.  A tile takes about 7,000,
+// because the staged rows fill the shared memory once (147 KB beside 74 KB of queries) and so the
+// parts take turns: the second product's first block, then staging (4,100 cycles for 147 KB by 11
+// warps: decoding runs at 52% of the issue slots, and the instruction cache is its next limit), then
+// what is left of the first product, then the softmax (1,200).  2 x 1,024 tokens of 64 heads over 15k
+// rows of MXFP4 take 6.0 ms: 740 TFLOP/s.  The same call on the way there:
+//   one warp per row and head, CUDA cores                                            812 ms
+//   CTA pairs, 128 rows x 128 keys, each staging half, halves exchanged               9.2 ms
+//   keys as M, one CTA for 64 rows (no exchange; the pair's took 5,500 cycles)        9.8 ms
+//   rolled staging and MMA loops (code within the instruction cache)                  8.5 ms
+//   MMAs issued from uniform registers, staging in rounds of three tasks              7.3 ms
+//   proxy fence at the reader, chunk 8 in the second round                            7.0 ms
+//   a chunk pair signalled as soon as it is staged, its products in one run           6.4 ms
+//   fewer registers live in staging and softmax, outputs stored by 16 bytes           6.0 ms
 #include <type_traits>
 
 #include "common.cuh"
@@ -426,11 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // Task (chunk pair, 8 keys): lane (key, q) decodes the q-th scale block of 32 channels of
         // the pair.  A key's four lanes read 64 bytes of its row; so that eight lanes of a store hold
         // eight different columns, the second chunk's blocks start with their upper half.  Warp w
-        // takes tasks w, w + 11, .., three a round: a round is one run of instructions with nothing
-        // to wait for inside (72 tasks with MMAs beside them took 2,770 cycles with six tasks a round,
-        // 3,750 with two).  Chunk 8 makes 16 tasks of half the size, spread so
-        // that each warp has about the same.  A round's rows of the next tile are on their way as
-        // soon as its registers are free; where they lie is read before it starts.
+        // takes tasks w, w + 11, .., three a round; the product before is waited for, and what is
+        // staged is signalled, between the tasks where that lets the other side start (a signal a
+        // round: 7.0 ms where this takes 6.4).  Chunk 8 makes 16 tasks of half the size, spread so
+        // that each warp has about the same.  Of 4-bit rows a round's codes of the next tile are on
+        // their way as soon as its registers are free; 8- and 16-bit rows are read as they are needed,
+        // since a tile ahead they would not fit the registers (MXFP8, 9 x 257 tokens over 4k rows:
+        // 1.48 ms, against 1.23).
         const int w = warp - kStageWarp, key8 = lane >> 2, q = lane & 3;
         const bool swap = q >= 2;
         const int j0 = w < 9 ? 6 + w : 3 * (w - 9), jn = w < 9 ? (w == 0 ? 2 : 1) : 3, jstep = w < 9 ? 9 : 1;

@@ -158,7 +158,8 @@ CSA2_API csa2_status csa2p_read(const csa2p_cache *cache, const int32_t *slot, i
 /* left as they were in out and lse.  Rows no query of a request sees are not read; a page    */
 /* id outside [0, n_pages), or a row past the table's width, sets CSA2_DEV_BAD_INDEX and its   */
 /* rows are no keys.  A cache row with a value or scale that is not finite makes the outputs   */
-/* of the queries that see it NaN, and of no others.                                          */
+/* of the queries that see it NaN, and of no others; scale bytes that could take a value past    */
+/* float32 (MXFP4 253 and up, MXFP8 247 and up: no quantised row has them) count as such.       */
 /* The codes of all pages may span up to 64 GB and their scales up to 4 GB (else UNSUPPORTED).  */
 /* Products are bf16 x bf16 with float32 sums; softmax weights are rounded to bf16 for the     */
 /* second product, their sum is float32.  cu has to be non-decreasing with cu[batch] <=        */
