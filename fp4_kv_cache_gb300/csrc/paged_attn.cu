@@ -384,6 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         int64_t own = 0, items;
         for (int b = b0; b < b1; ++b) own += row_tiles(P, b);
         int64_t at = block_scan(own, M.scan, items);
+        if (items > (int64_t)P.n_tokens * P.H / kRows + P.batch) {   // only of requests that overlap: none is done
+            items = 0;
+            if (tid == 0 && cta == 0) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+        }
         for (int b = b0; b < b1; ++b) {
             tiles_before[b] = (int32_t)at;
             at += row_tiles(P, b);

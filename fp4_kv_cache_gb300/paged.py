@@ -2,7 +2,8 @@
 
 As in ``csa2``: the helpers check what they are given, allocate outputs with torch and call the C
 entry points, and everything is computed by the library's kernels.  Work goes to the current
-CUDA stream (or the one given), on the current device, which has to be the tensors'.
+CUDA stream (or the one given: what a call allocates then belongs to that stream), on the current
+device, which has to be the tensors'.
 
 A decode step's calls take a few microseconds each on the GPU, so the way there is kept short:
 argument structures are packed with ``struct`` (the ctypes classes below name their fields and
@@ -114,6 +115,15 @@ def _maybe(t, name: str, dtype, n: Optional[int], dev: int) -> int:
     return 0 if t is None else _need(t, name, dtype, n, dev)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor of a call: of the given stream's memory, so that no block is written there that
+    another stream has not done with."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _status(d_status, dev: int):
     return None if d_status is None else _need(d_status, "d_status", _i32, None, dev)
 
@@ -188,7 +198,7 @@ def page_plan(lens, delta, block_table, free_pages, n_free, page: int, n_rows: i
     width = block_table.shape[1]
     if plan is None:
         # one allocation: lens | n_free | cu | slot | row_req | row_pos
-        buf = torch.empty(2 * B + 2 + 3 * n_rows, dtype=_i32, device=lens.device)
+        buf = _empty(2 * B + 2 + 3 * n_rows, _i32, lens.device, stream)
         parts = torch.split_with_sizes(buf, (B, 1, B + 1, n_rows, n_rows, n_rows))
         base = buf.data_ptr()
         at_cu, at_slot = base + 4 * B + 4, base + 8 * B + 8
@@ -245,7 +255,7 @@ def rope_axes(x, pos, cos_sin, sections: Optional[Sequence[int]] = None, out=Non
     if heads < 2:
         sh = d
     if out is None:
-        out = torch.empty((rows, heads, d), dtype=_bf16, device=x.device)
+        out = _empty((rows, heads, d), _bf16, x.device, stream)
         tr, th = heads * d, d
     else:
         if out.shape != x.shape or out.dtype is not _bf16 or out.get_device() != dev or out.stride(2) != 1:
@@ -279,7 +289,7 @@ def paged_read(cache: PagedCache, slot, out=None, d_status=None, stream=None):
     dev = cache._on_gpu()
     rows, d = slot.shape[0], cache.d
     if out is None:
-        out, ldo = torch.empty((rows, d), dtype=_bf16, device=cache.device), d
+        out, ldo = _empty((rows, d), _bf16, cache.device, stream), d
     else:
         if out.dtype is not _bf16 or out.get_device() != dev or out.shape != (rows, d) or out.stride(1) != 1:
             raise ValueError("out is a bf16 tensor [rows, d] on the cache's device with contiguous channels")
@@ -310,22 +320,21 @@ def paged_attn(q, cache: PagedCache, block_table, lens, cu, pos0=None, d_v: Opti
                    _maybe(kv_start, "kv_start", _i32, B, dev))
     at_out = _maybe(out, "out", _bf16, T * H * max(d_v, 0), dev)
     if out is None:
-        out = torch.empty((T, H, max(d_v, 0)), dtype=_bf16, device=cache.device)
+        out = _empty((T, H, max(d_v, 0)), _bf16, cache.device, stream)
         at_out = out.data_ptr()
     at_lse = _maybe(lse, "lse", _f32, T * H, dev)
     if lse is None and want_lse:
-        lse = torch.empty((T, H), dtype=_f32, device=cache.device)
+        lse = _empty((T, H), _f32, cache.device, stream)
         at_lse = lse.data_ptr()
     need = lib.csa2p_attn_workspace_size(a)
     raw = _stream_of(dev, stream)
     at_ws, size = 0, 0
     if workspace is not None:
-        at_ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        at_ws = _need(workspace, "workspace", workspace.dtype, None, dev)
+        size = workspace.numel() * workspace.element_size()
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        workspace = _empty(need, torch.uint8, cache.device, stream)
         at_ws, size = workspace.data_ptr(), need
-        if stream is not None:
-            workspace.record_stream(stream)
     st = lib.csa2p_attn(a, at_out, at_lse or None, at_ws or None, size, _status(d_status, dev), raw)
     if st:
         raise Csa2Error("csa2p_attn", st)

@@ -163,7 +163,8 @@ CSA2_API csa2_status csa2p_read(const csa2p_cache *cache, const int32_t *slot, i
 /* The codes of all pages may span up to 64 GB and their scales up to 4 GB (else UNSUPPORTED).  */
 /* Products are bf16 x bf16 with float32 sums; softmax weights are rounded to bf16 for the     */
 /* second product, their sum is float32.  cu has to be non-decreasing with cu[batch] <=        */
-/* n_tokens (what lies outside is left out).                                                  */
+/* n_tokens (what lies outside is left out; a call whose requests overlap so that they have     */
+/* more rows than q sets CSA2_DEV_BAD_INDEX and does nothing).                                  */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     csa2p_cache cache;

@@ -624,6 +624,46 @@ def test_attn_given_stream():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_given_stream_owns_what_a_call_allocates():
+    # a block that the current stream still writes is not handed to the other stream's call
+    x = torch.randn((512, 8, 128), device=DEV).bfloat16()
+    cs, pos = cos_sin(600, 32), ints(range(512))
+    want = paged.rope_axes(x, pos, cs)
+    s, big = torch.cuda.Stream(), torch.randn((4096, 4096), device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy = torch.empty_like(want)
+        for _ in range(20):
+            big = torch.tanh(big @ big)
+        busy.fill_(7.0)
+        del busy
+        got = paged.rope_axes(x, pos, cs, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_attn_refuses_workspace():
+    c = AttnCase([300], [2], 16, 128, 128, paged.MXFP4, 32, seed=20)
+    with pytest.raises(ValueError):
+        c.run(workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        c.run(workspace=torch.empty((2, 1 << 26), dtype=torch.uint8, device=DEV)[:, ::2])
+    with pytest.raises(paged.Csa2Error):
+        c.run(workspace=torch.empty(1024, dtype=torch.uint8, device=DEV))
+
+
+def test_attn_overlapping_requests():
+    # bounds that give the same rows to two requests: flagged, nothing written
+    c = AttnCase([40, 7, 33], [5, 0, 0], 64, 128, 128, paged.MXFP4, 32, seed=21)
+    c.cu = np.array([0, 5, 0, 5])
+    out = torch.full((5, 64, 128), 3.0, device=DEV).bfloat16()
+    lse = torch.full((5, 64), 3.0, device=DEV)
+    st = status()
+    c.run(st, out=out, lse=lse)
+    assert int(st) == csa2.DEV_BAD_INDEX
+    assert bool((out == 3.0).all()) and bool((lse == 3.0).all())
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("fmt", [paged.NVFP4_E4M3_16, paged.MXFP8])
 def test_steps_of_a_server(fmt):
