@@ -154,6 +154,9 @@ class PagedCache:
         for t in (codes, scales):
             if t is not None and not (t.stride(2) == 1 and t.stride(1) == t.shape[2]):
                 raise ValueError("rows must be contiguous within a page")
+            # an expanded tensor's stride of 0 would be taken for dense pages, past its storage
+            if t is not None and n > 1 and t.stride(0) < page * t.shape[2]:
+                raise ValueError("pages must not overlap")
         self.codes, self.scales, self.fmt, self.d, self.page, self.n_pages = codes, scales, fmt, d, page, n
         self.device = codes.device
         self.index = codes.get_device()               # -1: not on a GPU
