@@ -215,6 +215,11 @@ __device__ __forceinline__ void request_tokens(const AttnParams &P, int b, int32
     first = c0;
     tokens = c1 - c0;
 }
+// Requests that share rows: cu steps down within q.
+__device__ __forceinline__ bool steps_down(const AttnParams &P, int b)
+{
+    return min(max(P.cu[b + 1], 0), P.n_tokens) < min(max(P.cu[b], 0), P.n_tokens);
+}
 __device__ __forceinline__ int32_t row_tiles(const AttnParams &P, int b)
 {
     int32_t f, n;
@@ -382,9 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const int per = (P.batch + kThreads - 1) / kThreads;
         const int b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
         int64_t own = 0, items;
-        for (int b = b0; b < b1; ++b) own += row_tiles(P, b);
+        constexpr int64_t kDown = int64_t(1) << 40;        // more than all the tiles of a call
+        for (int b = b0; b < b1; ++b) own += row_tiles(P, b) + (steps_down(P, b) ? kDown : 0);
         int64_t at = block_scan(own, M.scan, items);
-        if (items > (int64_t)P.n_tokens * P.H / kRows + P.batch) {   // only of requests that overlap: none is done
+        if (items >= kDown) {                              // two CTAs would write the same rows: none is done
             items = 0;
             if (tid == 0 && cta == 0) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
         }

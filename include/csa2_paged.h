@@ -162,9 +162,9 @@ CSA2_API csa2_status csa2p_read(const csa2p_cache *cache, const int32_t *slot, i
 /* float32 (MXFP4 253 and up, MXFP8 247 and up: no quantised row has them) count as such.       */
 /* The codes of all pages may span up to 64 GB and their scales up to 4 GB (else UNSUPPORTED).  */
 /* Products are bf16 x bf16 with float32 sums; softmax weights are rounded to bf16 for the     */
-/* second product, their sum is float32.  cu has to be non-decreasing with cu[batch] <=        */
-/* n_tokens (what lies outside is left out; a call whose requests overlap so that they have     */
-/* more rows than q sets CSA2_DEV_BAD_INDEX and does nothing).                                  */
+/* second product, their sum is float32.  cu has to be non-decreasing: a call in which it        */
+/* steps down between 0 and n_tokens, so that requests could share rows of q, sets               */
+/* CSA2_DEV_BAD_INDEX and does nothing.  What lies outside 0..n_tokens is left out.             */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     csa2p_cache cache;
