@@ -151,19 +151,28 @@ class PagedCache:
             except KeyError:
                 raise ValueError("the widths of codes and scales fit no row format") from None
             d = w if fmt == MXFP8 else 2 * w
-        for t in (codes, scales):
-            if t is not None and not (t.stride(2) == 1 and t.stride(1) == t.shape[2]):
-                raise ValueError("rows must be contiguous within a page")
-            # an expanded tensor's stride of 0 would be taken for dense pages, past its storage
-            if t is not None and n > 1 and t.stride(0) < page * t.shape[2]:
-                raise ValueError("pages must not overlap")
+        code_pages, scale_pages = self._pages(codes, n, page, w), 0
+        if scales is not None:
+            scale_pages = self._pages(scales, n, page, scales.shape[2])
         self.codes, self.scales, self.fmt, self.d, self.page, self.n_pages = codes, scales, fmt, d, page, n
         self.device = codes.device
         self.index = codes.get_device()               # -1: not on a GPU
         self.fields = (fmt, d, page, n, codes.data_ptr(), scales.data_ptr() if scales is not None else 0,
-                       codes.stride(0) * codes.element_size() if n > 1 else 0,
-                       scales.stride(0) if scales is not None and n > 1 else 0)
+                       2 * code_pages if fmt == BF16 else code_pages, scale_pages)
         self.packed = _CACHE.pack(*self.fields)
+
+    @staticmethod
+    def _pages(t, n: int, page: int, w: int) -> int:
+        """Elements between pages; 0 where there is one."""
+        pages, rows, elements = t.stride()
+        if elements != 1 or rows != w:
+            raise ValueError("rows must be contiguous within a page")
+        if n < 2:
+            return 0
+        # an expanded tensor's stride of 0 would be taken for dense pages, past its storage
+        if pages < page * w:
+            raise ValueError("pages must not overlap")
+        return pages
 
     def _on_gpu(self) -> int:
         if self.index < 0:
