@@ -201,7 +201,7 @@ struct Item {                 // a row tile
     int32_t b, j;             // request, row tile of it
     int32_t rows;             // rows of the tile (1..64)
     int32_t len;              // rows of the cache that the table can reach
-    int64_t row0, p0;         // first row in q; position of the request's token 0
+    int64_t row0, p0;         // first row in q; position of the request's first token there
     int32_t lo, hi;           // keys that some row of the tile may see
     int32_t lo_all, hi_all;   // keys that every row of the tile sees
     int32_t nt;               // key tiles, from lo on (at least one, maybe of no key)
@@ -229,7 +229,8 @@ __device__ __forceinline__ int32_t row_tiles(const AttnParams &P, int b)
 // Keys [lo, hi) of the query at position p.
 __device__ __forceinline__ void bounds(const AttnParams &P, int64_t p, int32_t len, int32_t start, int32_t &lo, int32_t &hi, int64_t &end)
 {
-    const int64_t e = p < 0 ? 0 : P.ratio == 1 ? p + 1 : (uint32_t)(p + 1) / (uint32_t)P.ratio;   // p + 1 < 2^32
+    // (a position of 2^32 - 1 and up counts as that one; only offsets far below 0 lead there)
+    const int64_t e = p < 0 ? 0 : P.ratio == 1 ? p + 1 : (uint32_t)min(p + 1, (int64_t)0xffffffff) / (uint32_t)P.ratio;
     end = e;
     hi = (int32_t)(e < len ? e : len);
     int64_t l = start > 0 ? start : 0;
@@ -250,7 +251,9 @@ __device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
     const int32_t held = max(P.lens[b], 0);
     const int64_t reach = (int64_t)P.width << P.C.shift;
     it.len = (int32_t)(held < reach ? held : reach);
-    it.p0 = P.pos0 ? (int64_t)P.pos0[b] : (int64_t)held - tokens;
+    // Tokens that lie outside q count: those that are left keep their positions.
+    const int64_t c0 = P.cu[b];
+    it.p0 = (P.pos0 ? (int64_t)P.pos0[b] : held - (P.cu[b + 1] - c0)) + (first - c0);
     const int32_t start = P.start ? P.start[b] : 0;
     const uint32_t r0 = (uint32_t)j * kRows;               // rows of a call are fewer than 2^31
     const uint32_t t0 = r0 / (uint32_t)P.H, t1 = (r0 + it.rows - 1) / (uint32_t)P.H;

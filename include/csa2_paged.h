@@ -164,7 +164,8 @@ CSA2_API csa2_status csa2p_read(const csa2p_cache *cache, const int32_t *slot, i
 /* Products are bf16 x bf16 with float32 sums; softmax weights are rounded to bf16 for the     */
 /* second product, their sum is float32.  cu has to be non-decreasing: a call in which it        */
 /* steps down between 0 and n_tokens, so that requests could share rows of q, sets               */
-/* CSA2_DEV_BAD_INDEX and does nothing.  What lies outside 0..n_tokens is left out.             */
+/* CSA2_DEV_BAD_INDEX and does nothing.  Tokens outside 0..n_tokens are left out; the    */
+/* request's others keep their positions.                                                       */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     csa2p_cache cache;

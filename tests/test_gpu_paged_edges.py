@@ -35,3 +35,35 @@ def test_attn_offsets_outside_do_not_step_down(cu):
     c.cu, st = np.array(cu), status()
     got, _ = c.run(st)
     assert torch.equal(got, want) and int(st) == 0
+
+
+@pytest.mark.parametrize("front,back", [(0, 4), (4, 0), (3, 5)])
+@pytest.mark.parametrize("window,ratio,pos0", [(0, 1, None), (5, 1, None), (0, 1, [97, 46]), (7, 2, [180, 100])])
+def test_attn_queries_cut_off(front, back, window, ratio, pos0):
+    # offsets that reach past q at either end: the tokens that q holds keep their positions
+    c = AttnCase([100, 60], [7, 10], 16, 128, 128, paged.MXFP4, 16, window, ratio, pos0, seed=23)
+    o, l, ob, lb = c.ref()
+    keep = slice(front, 17 - back)
+    c.q, c.cu, st = c.q[keep].contiguous(), c.cu - front, status()
+    out, lse = c.run(st)
+    close(out, o[keep], ob[keep])
+    close(lse, l[keep], lb[keep])
+    assert int(st) == 0
+
+
+def test_layer_with_more_rows_than_it_is_given():
+    # a step of ten new rows, six of them given: flagged, and the six attend what they would have
+    H, d, page, fmt = 16, 128, 16, paged.MXFP8
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x, q = torch.randn((30, d), generator=g, device=DEV).bfloat16(), torch.randn((30, H, d), generator=g, device=DEV).bfloat16()
+    cs, got = cos_sin(100, 32), []
+    for T in (10, 6):
+        cache = paged.PagedCache.new(8, page, d, fmt)
+        cache.scales.fill_(127)
+        state = layers.PagedState(ints([0]), ints([[-1] * 4]), ints(range(8)), ints([8]))
+        layers.paged_layer(cache, state, layers.PagedInput(q[:20], x[:20], ints([20]), cs), d_v=128)
+        cache.codes[int(state.block_table[0, 1]), 4:] = 0x70     # what the page held before: not to be seen
+        st = status()
+        got.append(layers.paged_layer(cache, state, layers.PagedInput(q[20:20 + T], x[20:20 + T], ints([10]), cs), d_v=128, d_status=st))
+        assert int(st) == (0 if T == 10 else paged.DEV_ROWS)
+    assert torch.equal(got[1].out, got[0].out[:6]) and torch.equal(got[1].lse, got[0].lse[:6])
