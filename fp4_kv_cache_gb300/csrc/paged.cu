@@ -54,37 +54,13 @@ __device__ __forceinline__ int last_at_or_below(const int32_t *a, int n, int32_t
 
 __device__ __forceinline__ int32_t hold31(int64_t v) { return (int32_t)(v > 0x7fffffff ? 0x7fffffff : v); }
 
-// Every CTA scans all the requests for itself -- rows added, pages taken, pages given back -- so
-// that the rows, the taken pages and the returned pages can be shared out with no exchange.  No
-// CTA writes what another may still read: table entries read are never written (a request takes or
-// gives back, not both), and the free list is read below n_free and written above it.  Only the new
-// lengths and count may go where the old ones are: then (`later`) a second kernel writes them, and
-// with one CTA a barrier is enough.  What bounds it is the chain of loads, scans and barriers, not
-// its bytes: 512 requests of one new row take 6.7 us, 193 with room for 65,536 new rows 9.8 us.
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams P, const int later, uint32_t *d_status)
+// Exclusive sums of K numbers a thread over the block.
+template <int K>
+__device__ __forceinline__ void block_before(const int64_t (&own)[K], int64_t (&before)[K], int64_t (*s_warp)[32])
 {
-    extern __shared__ int32_t sm[];
-    int32_t *s_cu = sm, *s_take = s_cu + P.batch + 1, *s_back = s_take + P.batch + 1;
-    __shared__ int64_t s_warp[3][32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_cta = gridDim.x, cta = blockIdx.x;
-    pdl_wait();
-    pdl_allow_dependents();
-    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
-    // ---- scan of the requests, `per` consecutive ones a thread
-    const int per = (P.batch + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
-    int64_t own[3] = {0, 0, 0};
-    for (int b = b0; b < b1; ++b) {
-        const Req r = plan_req(P, b);
-        own[0] += r.new_len > r.old_len ? r.new_len - r.old_len : 0;
-        own[1] += max(r.has - r.had, 0);
-        own[2] += max(r.had - r.has, 0);
-        if (r.full && cta == 0) dev_flag(d_status, CSA2P_DEV_TABLE_FULL);
-    }
-    int64_t before[3];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < K; ++k) {
         int64_t v = own[k];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -95,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
         before[k] = v - own[k];
     }
     __syncthreads();
-    if (warp < 3) {
+    if (warp < K) {
         int64_t v = lane < kPlanThreads / 32 ? s_warp[warp][lane] : 0;
         const int64_t mine = v;
 #pragma unroll
@@ -107,13 +83,81 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 3; ++k) before[k] += s_warp[k][warp];
+    for (int k = 0; k < K; ++k) before[k] += s_warp[k][warp];
+}
+
+// What the requests before each (and, last, all of them) add and move: [batch + 1] in shared memory.
+struct PlanSums {
+    int32_t *cu, *take, *back;      // rows added, pages taken, pages given back
+};
+
+// Entries that request b (threads without one: has = had = 0) gives back and that name a page.
+// Called by whole warps: a thread counts a few entries itself, all 32 those of a request with many.
+__device__ __forceinline__ int32_t pages_named(const PlanParams &P, int b, const Req &r)
+{
+    constexpr int32_t kFew = 4;
+    const int lane = threadIdx.x & 31;
+    const int32_t n = max(r.had - r.has, 0);
+    int32_t count = 0;
+#pragma unroll
+    for (int32_t i = 0; i < kFew; ++i)
+        if (n <= kFew && i < n) count += P.table[(int64_t)b * P.width + r.has + i] >= 0;
+    uint32_t many = __ballot_sync(0xffffffffu, n > kFew);
+    while (many) {
+        const int from = __ffs((int)many) - 1;
+        many &= many - 1;
+        const int32_t *t = P.table + (int64_t)__shfl_sync(0xffffffffu, b, from) * P.width + __shfl_sync(0xffffffffu, r.has, from);
+        const int32_t m = __shfl_sync(0xffffffffu, n, from);
+        int32_t c = 0;
+#pragma unroll 8
+        for (int32_t i = lane; i < m; i += 32) c += t[i] >= 0;
+        c = (int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)c);
+        if (lane == from) count = c;
+    }
+    return count;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas()
+{
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void set_peer(int32_t *p, uint32_t rank)      // the peer's copy of shared *p: 1
+{
+    uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n\tst.shared::cluster.b32 [%0], %2;" : "+r"(at) : "r"(rank), "r"(1) : "memory");
+}
+
+// Scans the requests, `per` consecutive ones a thread; entries given back are taken for pages.  One
+// CTA tells (cu, status).
+__device__ __forceinline__ void plan_scan(const PlanParams &P, const PlanSums &S, int64_t (*s_warp)[32], bool tell, uint32_t *d_status)
+{
+    const int per = (P.batch + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min((int)threadIdx.x * per, P.batch), b1 = min(b0 + per, P.batch);
+    int64_t own[3] = {0, 0, 0}, before[3];
+    for (int b = b0; b < b1; ++b) {
+        const Req r = plan_req(P, b);
+        own[0] += r.new_len > r.old_len ? r.new_len - r.old_len : 0;
+        own[1] += max(r.has - r.had, 0);
+        own[2] += max(r.had - r.has, 0);
+        if (r.full && tell) dev_flag(d_status, CSA2P_DEV_TABLE_FULL);
+    }
+    block_before<3>(own, before, s_warp);
     for (int b = b0; b <= b1; ++b) {
         if (b == b1 && b != P.batch) break;                    // the next thread's first entry
-        s_cu[b] = hold31(before[0]);
-        s_take[b] = hold31(before[1]);
-        s_back[b] = hold31(before[2]);
-        if (cta == 0) P.cu[b] = s_cu[b];
+        S.cu[b] = hold31(before[0]);
+        S.take[b] = hold31(before[1]);
+        S.back[b] = hold31(before[2]);
+        if (tell) P.cu[b] = S.cu[b];
         if (b == b1) break;
         const Req r = plan_req(P, b);
         before[0] += r.new_len > r.old_len ? r.new_len - r.old_len : 0;
@@ -121,6 +165,116 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
         before[2] += max(r.had - r.has, 0);
     }
     __syncthreads();
+}
+
+// Whether one of this thread's share of the entries given back names no page.  The cluster's CTAs share
+// the entries out, 512 a warp, so that sixteen loads of a thread follow one another.
+__device__ __forceinline__ bool plan_look(const PlanParams &P, const PlanSums &S, uint32_t rank, uint32_t peers)
+{
+    constexpr int kEach = 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t all = S.back[P.batch];
+    int32_t seen = 0;
+    for (int64_t i0 = 32ll * kEach * (rank * (kPlanThreads / 32) + warp); i0 < all; i0 += (int64_t)kEach * kPlanThreads * peers) {
+        const int32_t *p[kEach];
+        int b = last_at_or_below(S.back, P.batch, (int32_t)min(i0 + lane, (int64_t)all - 1));
+        int32_t at = S.back[b], end = S.back[b + 1];
+        const int32_t *t = P.table + (int64_t)b * P.width + plan_req(P, b).has;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int32_t i = (int32_t)min(i0 + lane + 32 * k, (int64_t)all - 1);
+            if (i >= end) {
+                while (S.back[b + 1] <= i) ++b;                // i < back[batch]: ends in time
+                at = S.back[b];
+                end = S.back[b + 1];
+                t = P.table + (int64_t)b * P.width + plan_req(P, b).has;
+            }
+            p[k] = t + (i - at);
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) seen |= *p[k];
+    }
+    return seen < 0;
+}
+
+// Counts the pages given back anew: those that the entries name.
+__device__ __noinline__ void plan_recount(const PlanParams &P, const PlanSums &S, int64_t (*s_warp)[32])
+{
+    const int per = (P.batch + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min((int)threadIdx.x * per, P.batch), b1 = min(b0 + per, P.batch);
+    int64_t named[1] = {0}, first[1];
+    for (int k = 0; k < per; ++k) {                            // whole warps: pages_named
+        const int b = b0 + k;
+        Req r = {};
+        if (b < b1) r = plan_req(P, b);
+        const int32_t n = pages_named(P, b, r);
+        if (b < b1) S.back[b] = n;
+        named[0] += n;
+    }
+    block_before<1>(named, first, s_warp);
+    for (int b = b0; b <= b1; ++b) {
+        if (b == b1 && b != P.batch) break;
+        const int32_t n = b < b1 ? S.back[b] : 0;
+        S.back[b] = hold31(first[0]);
+        first[0] += n;
+    }
+    __syncthreads();
+}
+
+// One block: all old lengths are read before the first new one is written.
+__device__ __forceinline__ void new_lengths(const PlanParams &P, int32_t n_out)
+{
+    int32_t len_new[kPlanMaxReq];
+#pragma unroll
+    for (int k = 0; k < kPlanMaxReq; ++k) {
+        const int b = threadIdx.x + k * kPlanThreads;
+        if (b < P.batch) len_new[k] = (int32_t)plan_req(P, b).new_len;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPlanMaxReq; ++k) {
+        const int b = threadIdx.x + k * kPlanThreads;
+        if (b < P.batch) P.lens_out[b] = len_new[k];
+    }
+    if (threadIdx.x == 0) P.n_free_out[0] = n_out;
+}
+
+// Every CTA scans all the requests for itself -- rows added, pages taken, pages given back -- so
+// that the rows, the taken pages and the returned pages can be shared out with no exchange.  No
+// CTA writes what another may still read: table entries read are never written (a request takes or
+// gives back, not both), and the free list is read below n_free and written above it.  Only the new
+// lengths and count may go where the old ones are: then (`later`) a second kernel writes them, and
+// with one CTA a barrier is enough.  A shortage leaves -1 in a table, which is no page to give back:
+// the entries given back are looked at, shared out over the CTAs of a cluster, and counted only where
+// one names no page.  What bounds it is the chain of loads, scans and barriers, not its bytes: 512
+// requests of one new row take 7.1 us, 193 with room for 65,536 new rows and 30,000 pages given back
+// 13.9 us (9.9 without the look; 16.7 with each CTA looking at all of them).
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams P, const int later, uint32_t *d_status)
+{
+    extern __shared__ int32_t sm[];
+    int32_t *s_cu = sm, *s_take = s_cu + P.batch + 1, *s_back = s_take + P.batch + 1;
+    __shared__ int64_t s_warp[3][32];
+    __shared__ int32_t s_hole;
+    const int tid = threadIdx.x, n_cta = gridDim.x, cta = blockIdx.x;
+    const uint32_t peers = cluster_ctas();
+    if (tid == 0) s_hole = 0;
+    if (peers > 1) cluster_arrive();
+    pdl_wait();
+    pdl_allow_dependents();
+    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
+    const PlanSums S{s_cu, s_take, s_back};
+    plan_scan(P, S, s_warp, cta == 0, d_status);
+    if (peers > 1) cluster_wait();                             // the peers' marks are clear
+    if (s_back[P.batch] > 0) {
+        bool hole = __syncthreads_or(plan_look(P, S, cluster_rank(), peers));
+        if (peers > 1) {
+            if (hole && tid < peers) set_peer(&s_hole, tid);
+            cluster_arrive();
+            cluster_wait();
+            hole = *(volatile int32_t *)&s_hole;
+        }
+        if (hole) plan_recount(P, S, s_warp);
+    }
     const int n_new = s_cu[P.batch], n_take = s_take[P.batch], n_back = s_back[P.batch];
     const int64_t top = (int64_t)n_free + n_back;
     if (tid == 0 && cta == 0) {
@@ -130,7 +284,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     }
     auto returned = [&](int i) -> int32_t {                    // i-th page given back
         const int b = last_at_or_below(s_back, P.batch, i);
-        return P.table[(int64_t)b * P.width + plan_req(P, b).has + (i - s_back[b])];
+        const Req r = plan_req(P, b);
+        const int32_t *t = P.table + (int64_t)b * P.width + r.has;
+        int32_t k = i - s_back[b];
+        const int32_t n = r.had - r.has;
+        if (s_back[b + 1] - s_back[b] == n) return t[k];
+        for (int32_t j = 0; j < n; ++j)                        // some entries are no pages: the k-th that is
+            if (t[j] >= 0 && k-- == 0) return t[j];
+        return -1;
     };
     auto taken = [&](int i) -> int32_t {                       // i-th page handed out
         const int64_t at = top - 1 - i;
@@ -179,52 +340,21 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     const int64_t left = top - n_take < 0 ? 0 : top - n_take;
     for (int64_t i = first; i < n_back; i += step)
         if (n_free + i < left && n_free + i < P.free_cap) P.free_pages[n_free + i] = returned((int)i);
-    if (later || cta > 0) return;
-    int32_t len_new[kPlanMaxReq];
-#pragma unroll
-    for (int k = 0; k < kPlanMaxReq; ++k)
-        if (b0 + k < b1) len_new[k] = (int32_t)plan_req(P, b0 + k).new_len;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kPlanMaxReq; ++k)
-        if (b0 + k < b1) P.lens_out[b0 + k] = len_new[k];
-    if (tid == 0) P.n_free_out[0] = (int32_t)(left < P.free_cap ? left : P.free_cap);
+    if (cta > 0) return;
+    const int32_t n_out = (int32_t)(left < P.free_cap ? left : P.free_cap);
+    if (!later) new_lengths(P, n_out);
+    else if (tid == 0) P.cu[0] = n_out;                        // carried over to the second kernel
 }
 
-// The new lengths and count, when they overwrite the old ones: one block, all read before any is
-// written.  The count follows from the pages that the requests take and give back.
+// The new lengths and count, when they overwrite the old ones and several CTAs read those.  One
+// block.  The count comes in cu[0], which is 0 otherwise.
 __global__ void __launch_bounds__(kPlanThreads) page_plan_later_kernel(const PlanParams P)
 {
-    __shared__ int64_t s_warp[kPlanThreads / 32];
-    const int tid = threadIdx.x;
     pdl_wait();
     pdl_allow_dependents();
-    const int n_free = min(max(P.n_free[0], 0), P.free_cap);
-    int64_t grown = 0;
-    int32_t len_new[kPlanMaxReq];
-#pragma unroll
-    for (int k = 0; k < kPlanMaxReq; ++k) {
-        const int b = tid + k * kPlanThreads;
-        if (b < P.batch) {
-            const Req r = plan_req(P, b);
-            len_new[k] = (int32_t)r.new_len;
-            grown += r.has - r.had;
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) grown += __shfl_xor_sync(0xffffffffu, grown, o);
-    if ((tid & 31) == 0) s_warp[tid >> 5] = grown;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kPlanMaxReq; ++k) {
-        const int b = tid + k * kPlanThreads;
-        if (b < P.batch) P.lens_out[b] = len_new[k];
-    }
-    if (tid == 0) {
-        int64_t left = n_free;
-        for (int w = 0; w < kPlanThreads / 32; ++w) left -= s_warp[w];
-        P.n_free_out[0] = (int32_t)(left < 0 ? 0 : left < P.free_cap ? left : P.free_cap);
-    }
+    const int32_t n_out = P.cu[0];
+    new_lengths(P, n_out);
+    if (threadIdx.x == 0) P.cu[0] = 0;
 }
 
 // ---------------------------------------------------------------- rotation
@@ -610,12 +740,13 @@ cudaError_t launch_page_plan(const csa2p_plan_args &a, uint32_t *d_status, cudaS
         const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    // four rows a thread; few rows: one CTA, which needs no second kernel
+    // four rows a thread; few rows: one CTA, which needs no second kernel, else clusters of eight
     int64_t ctas = ((int64_t)a.n_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    if (ctas < 1) ctas = 1;
     if (ctas > device_sm_count()) ctas = device_sm_count();
+    const int cluster = ctas > 1 ? 8 : 1;
+    ctas = ctas > 1 ? (ctas + cluster - 1) / cluster * cluster : 1;
     const bool later = ctas > 1 && (a.lens_out == a.lens || a.n_free_out == a.n_free);
-    const cudaError_t e = launch_pdl(page_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, s, 1, P, later ? 1 : 0, d_status);
+    const cudaError_t e = launch_pdl(page_plan_kernel, dim3((unsigned)ctas), dim3(kPlanThreads), smem, s, cluster, P, later ? 1 : 0, d_status);
     if (e != cudaSuccess || !later) return e;
     return launch_pdl(page_plan_later_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, P);
 }

@@ -75,9 +75,10 @@ typedef struct {
 /* A page that the free list cannot supply is -1, and so are the slots in it             */
 /* (CSA2P_DEV_NO_PAGES); positions past the table's width have slot -1 and take no page   */
 /* (CSA2P_DEV_TABLE_FULL); rows past n_rows are dropped (CSA2P_DEV_ROWS).  A table entry  */
-/* below 0 gives slot -1.  lens below 0 counts as 0, lens + delta is held to 0..2^31-1.   */
-/* lens_out may be lens and n_free_out may be n_free: the call is replayed in a captured   */
-/* graph by updating delta alone.                                                        */
+/* below 0 gives slot -1, and is passed over when its request gives it back.              */
+/* lens below 0 counts as 0, lens + delta is held to 0..2^31-1.  lens_out may be lens and  */
+/* n_free_out may be n_free: the call is replayed in a captured graph by updating delta    */
+/* alone.                                                                                 */
 /* ---------------------------------------------------------------------------------- */
 #define CSA2P_MAX_BATCH 16384
 typedef struct {

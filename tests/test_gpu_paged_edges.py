@@ -12,6 +12,70 @@ from test_gpu_paged import AttnCase, DEV, FMTS, I32, check, close, cos_sin, ints
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------ bookkeeping
+def plan_step(lens, delta, table, stack, page):
+    """One step on lists: lens and table are updated, the stack of free pages is popped and pushed."""
+    new = [max(n + d, 0) for n, d in zip(lens, delta)]
+    had, has = ([-(-n // page) for n in v] for v in (lens, new))
+    for row, a, z in zip(table, has, had):
+        stack += [p for p in row[a:max(a, z)] if p >= 0]
+    short = False
+    for row, a, z in zip(table, had, has):
+        for j in range(a, z):
+            short |= not stack
+            row[j] = stack.pop() if stack else -1
+    slots = [row[p // page] * page + p % page if row[p // page] >= 0 else -1
+             for row, n, m in zip(table, lens, new) for p in range(n, m)]
+    lens[:] = new
+    return slots, paged.DEV_NO_PAGES if short else 0
+
+
+def run_plan(steps, lens, table, free, n_pages, page, n_rows, in_place):
+    """The steps on the GPU beside plan_step; every page stays either free or in one table."""
+    width = len(table[0])
+    t_lens, t_table, t_n = ints(lens), ints(table), ints([len(free)])
+    t_free = ints(free + [-9] * (n_pages - len(free)))
+    for delta in steps:
+        before, st = list(lens), status()
+        slots, want = plan_step(lens, delta, table, free, page)
+        p = paged.page_plan(t_lens, ints(delta), t_table, t_free, t_n, page, n_rows, in_place=in_place, d_status=st)
+        assert int(st) == want and p.lens.tolist() == lens
+        assert t_table.tolist() == table and int(p.n_free) == len(free) and t_free.tolist()[:len(free)] == free
+        assert p.slot.tolist() == slots + [-1] * (n_rows - len(slots))
+        held = [v for row, n in zip(table, lens) for v in row[:-(-n // page)] if v >= 0]
+        assert sorted(held + free) == list(range(n_pages))
+        if in_place:
+            assert t_lens.tolist() == lens and int(t_n) == len(free)
+        else:
+            assert t_lens.tolist() == before
+            t_lens, t_n = p.lens.clone(), p.n_free.clone()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_rows", [8, 5000])                             # one CTA, and several
+def test_plan_after_a_shortage(n_rows, in_place):
+    # a request starves, is taken back, and another asks: it gets the page that is free
+    run_plan([[0, 8], [0, -8], [0, 4], [-4, 0], [8, 0]], [4, 0], [[0, -1, -1], [-1, -1, -1]], [1], 2, 4, n_rows, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,page,n_pages,most,n_rows,seed", [
+    (3, 4, 6, 12, 64, 0), (9, 1, 60, 40, 400, 1), (9, 4, 90, 300, 3000, 2), (70, 16, 200, 400, 30000, 3), (700, 2, 900, 9, 7000, 4),
+    (40, 1, 900, 200, 8000, 5)])
+def test_plan_steps_with_shortages(B, page, n_pages, most, n_rows, seed, in_place):
+    # too few pages all the time: requests grow past the free list, shrink across its holes and end
+    r = np.random.default_rng(seed)
+    lens, steps = [0] * B, []
+    for _ in range(12):
+        grow = r.integers(0, most + 1, B)
+        back = -np.minimum(lens, r.choice([1, page + 1, most // 2 + 1, 10**6], B))
+        d = np.where(r.random(B) < 0.4, back, np.where(np.array(lens) > 3 * most, 0, grow))
+        steps.append([int(v) for v in d])
+        lens = [n + int(v) for n, v in zip(lens, d)]
+    width = 4 * most // page + 2
+    run_plan(steps, [0] * B, [[-1] * width for _ in range(B)], list(range(n_pages)), n_pages, page, n_rows, in_place)
+
+
 # ------------------------------------------------------------------ offsets of the queries
 @pytest.mark.parametrize("H", [1, 16, 64])
 @pytest.mark.parametrize("cu", [[0, 5, 0, 5], [0, 3, 1, 5], [0, 3, 1, 2], [5, 0, 5, 5], [0, 7, 4, 9], [2, -1, 3, 5]])
