@@ -226,16 +226,15 @@ __device__ __forceinline__ int32_t row_tiles(const AttnParams &P, int b)
     request_tokens(P, b, f, n);
     return (int32_t)(((int64_t)n * P.H + kRows - 1) / kRows);
 }
-// Keys [lo, hi) of the query at position p.
-__device__ __forceinline__ void bounds(const AttnParams &P, int64_t p, int32_t len, int32_t start, int32_t &lo, int32_t &hi, int64_t &end)
+// Keys [lo, hi) of the query at position p; none where lo >= hi.  Neither decreases with p.
+__device__ __forceinline__ void bounds(const AttnParams &P, int64_t p, int32_t len, int32_t start, int64_t &lo, int32_t &hi, int64_t &end)
 {
     // (a position of 2^32 - 1 and up counts as that one; only offsets far below 0 lead there)
     const int64_t e = p < 0 ? 0 : P.ratio == 1 ? p + 1 : (uint32_t)min(p + 1, (int64_t)0xffffffff) / (uint32_t)P.ratio;
     end = e;
     hi = (int32_t)(e < len ? e : len);
-    int64_t l = start > 0 ? start : 0;
-    if (P.window > 0 && e - P.window > l) l = e - P.window;
-    lo = (int32_t)(l < hi ? l : hi);
+    lo = start > 0 ? start : 0;
+    if (P.window > 0 && e - P.window > lo) lo = e - P.window;
 }
 __device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
 {
@@ -257,9 +256,11 @@ __device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
     const int32_t start = P.start ? P.start[b] : 0;
     const uint32_t r0 = (uint32_t)j * kRows;               // rows of a call are fewer than 2^31
     const uint32_t t0 = r0 / (uint32_t)P.H, t1 = (r0 + it.rows - 1) / (uint32_t)P.H;
-    int64_t e0, e1;
-    bounds(P, it.p0 + t0, it.len, start, it.lo, it.hi_all, e0);
-    bounds(P, it.p0 + t1, it.len, start, it.lo_all, it.hi, e1);
+    int64_t e0, e1, l0, l1;
+    bounds(P, it.p0 + t0, it.len, start, l0, it.hi_all, e0);
+    bounds(P, it.p0 + t1, it.len, start, l1, it.hi, e1);
+    it.lo = (int32_t)min(l0, (int64_t)it.hi);              // rows before the first query's are not read,
+    it.lo_all = (int32_t)min(l1, (int64_t)it.hi);          // even where it sees none itself
     it.beyond = held > it.len && e1 > it.len;
     // The first tile begins with the first key, so that a window of 128 is one tile (8 x 256 tokens
     // of 64 heads, MXFP8: 189 us; 308 with two tiles that begin at multiples of 128).
@@ -717,11 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (walk.first()) {
                 ++ib;
                 if (key_in < kRows) {                 // rows past the last: as the last
-                    int32_t lo, hi;
-                    int64_t e;
+                    int32_t hi;
+                    int64_t lo, e;
                     const uint32_t f = (uint32_t)walk.it.j * kRows + min(key_in, walk.it.rows - 1);
                     bounds(P, walk.it.p0 + f / (uint32_t)P.H, walk.it.len, P.start ? P.start[walk.it.b] : 0, lo, hi, e);
-                    M.lo[ib & 3][key_in] = lo;
+                    M.lo[ib & 3][key_in] = (int32_t)min(lo, (int64_t)hi);
                     M.hi[ib & 3][key_in] = hi;
                 }
                 if (key_in == 0) {

@@ -131,3 +131,13 @@ def test_layer_with_more_rows_than_it_is_given():
         got.append(layers.paged_layer(cache, state, layers.PagedInput(q[20:20 + T], x[20:20 + T], ints([10]), cs), d_v=128, d_status=st))
         assert int(st) == (0 if T == 10 else paged.DEV_ROWS)
     assert torch.equal(got[1].out, got[0].out[:6]) and torch.equal(got[1].lse, got[0].lse[:6])
+
+
+# ------------------------------------------------------------------ rows that no query sees
+@pytest.mark.parametrize("H,page,start,pos0,ratio", [
+    (1, 16, 100, None, 1), (16, 1, 101, None, 1), (64, 1, 37, [0], 1), (3, 4, 60, [5], 1), (2, 8, 90, [0], 2), (1, 16, 1000, None, 1)])
+def test_attn_leading_pages_given_up(H, page, start, pos0, ratio):
+    # a chunk from before kv_start: the pages in front of it are gone, and nobody asks for them
+    c = AttnCase([200], [200], H, 128, 128, paged.MXFP4, page, 0, ratio, pos0, [start], seed=24)
+    c.table[0, :start // page] = -1
+    check(c)
