@@ -206,7 +206,7 @@ struct Item {                 // a row tile
     int32_t lo_all, hi_all;   // keys that every row of the tile sees
     int32_t nt;               // key tiles, from lo on (at least one, maybe of no key)
     bool more;                // the request has further row tiles
-    bool beyond;              // some visible row lies past the table
+    bool beyond;              // rows past the table may be visible
 };
 
 __device__ __forceinline__ void request_tokens(const AttnParams &P, int b, int32_t &first, int32_t &tokens)
@@ -724,9 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     bounds(P, walk.it.p0 + f / (uint32_t)P.H, walk.it.len, P.start ? P.start[walk.it.b] : 0, lo, hi, e);
                     M.lo[ib & 3][key_in] = (int32_t)min(lo, (int64_t)hi);
                     M.hi[ib & 3][key_in] = hi;
+                    if (walk.it.beyond && min((int64_t)P.lens[walk.it.b], e) > max((int64_t)walk.it.len, lo))
+                        dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
                 }
                 if (key_in == 0) {
-                    if (walk.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
                     prefetch_l2(P.q + walk.it.row0 * P.C.d, walk.it.rows * P.C.d * 2);
                 }
             }

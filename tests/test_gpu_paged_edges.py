@@ -141,3 +141,21 @@ def test_attn_leading_pages_given_up(H, page, start, pos0, ratio):
     c = AttnCase([200], [200], H, 128, 128, paged.MXFP4, page, 0, ratio, pos0, [start], seed=24)
     c.table[0, :start // page] = -1
     check(c)
+
+
+@pytest.mark.parametrize("lens,pos0,window,start,flagged", [
+    (320, [400], 5, None, False),        # windows past all the rows held
+    (320, [300], 0, [400], False),       # kv_start past them
+    (320, [316], 3, None, True), (320, [303], 5, None, True), (320, [300], 5, None, False), (320, [301], 5, None, True),
+    (320, [321], 5, None, True), (320, [324], 5, None, False), (310, [300], 0, [306], False), (310, [303], 0, [306], True)])
+def test_attn_rows_past_the_table_that_none_sees(lens, pos0, window, start, flagged):
+    # the table reaches 304 rows: rows past it are flagged where a query would see them, and only there
+    c = AttnCase([304], [4], 16, 128, 128, paged.MXFP4, 16, window, 1, pos0, start, seed=25)
+    c.table, c.lens = c.table[:, :19], [lens]
+    seen = [range(max(start[0] if start else 0, p + 1 - window if window else 0), min(lens, p + 1)) for p in range(pos0[0], pos0[0] + 4)]
+    assert flagged == any(r.stop > 304 and len(r) for r in seen)
+    st = status()
+    out, lse = c.run(st)
+    assert int(st) == (csa2.DEV_BAD_INDEX if flagged else 0)
+    empty = torch.tensor([r.start >= min(r.stop, 304) for r in seen], device=DEV)
+    assert torch.equal((lse == -math.inf).all(1), empty) and bool((out[empty] == 0).all())
