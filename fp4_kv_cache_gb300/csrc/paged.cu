@@ -737,7 +737,7 @@ cudaError_t launch_page_plan(const csa2p_plan_args &a, uint32_t *d_status, cudaS
     P.row_pos = a.row_pos;
     const size_t smem = 3 * sizeof(int32_t) * ((size_t)a.batch + 1);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(page_plan_kernel), 3 * (int)sizeof(int32_t) * (CSA2P_MAX_BATCH + 1));
         if (e != cudaSuccess) return e;
     }
     // four rows a thread; few rows: one CTA, which needs no second kernel, else clusters of eight

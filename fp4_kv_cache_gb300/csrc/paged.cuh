@@ -36,6 +36,10 @@ struct RopeView {
 
 bool paged_view(const csa2p_cache &c, PagedView &v);    // false: not a valid cache
 
+// Shared memory beyond the default has to be asked for once per kernel and device.  The limit is the
+// kernel's own, for every thread of the process: always the same number of bytes for a kernel.
+cudaError_t allow_smem(const void *kernel, int bytes);
+
 cudaError_t launch_page_plan(const csa2p_plan_args &a, uint32_t *d_status, cudaStream_t s);
 cudaError_t launch_paged_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_t *out, int64_t out_row,
                               int64_t out_head, int32_t rows, int32_t heads, int32_t d, const RopeView &rope,

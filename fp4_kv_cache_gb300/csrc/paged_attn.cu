@@ -1052,10 +1052,11 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(const __grid_const
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Shared memory beyond the default has to be asked for once per kernel and device.
+} // namespace
+
 cudaError_t allow_smem(const void *kernel, int bytes)
 {
-    constexpr int kMaxDevices = 64, kKernels = 8;
+    constexpr int kMaxDevices = 64, kKernels = 12;
     static std::atomic<const void *> done[kMaxDevices][kKernels];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1072,6 +1073,8 @@ cudaError_t allow_smem(const void *kernel, int bytes)
     }
     return cudaSuccess;
 }
+
+namespace {
 
 template <bool FULL>
 auto attn_kernel(int fmt) -> void (*)(AttnParams)

@@ -1,6 +1,7 @@
 """Paged-cache calls at their edges: steps after a shortage of pages, offsets that step down or leave
 the queries, masks that leave leading pages unread, rows that are not finite, calls at once."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -74,6 +75,33 @@ def test_plan_steps_with_shortages(B, page, n_pages, most, n_rows, seed, in_plac
         lens = [n + int(v) for n, v in zip(lens, d)]
     width = 4 * most // page + 2
     run_plan(steps, [0] * B, [[-1] * width for _ in range(B)], list(range(n_pages)), n_pages, page, n_rows, in_place)
+
+
+def test_plans_of_two_sizes_at_once():
+    # two host threads, each with its own stream: the larger plan's shared memory is not taken away
+    lib, calls, bad = paged._lib(), [], []
+    for B in (paged.MAX_BATCH, 4000):
+        buf, s = torch.zeros(8 * B + 64, dtype=I32, device=DEV), torch.cuda.Stream()
+        at = [buf.data_ptr() + 4 * (i * B + 4 * i) for i in range(6)]   # lens, delta, new lens, table, cu, the rest
+        args = paged._PLAN.pack(B, 16, 1, 4, 4, at[0], at[1], at[2], at[3], at[5], at[5] + 32, at[5] + 64, at[4], at[5] + 96,
+                                at[5] + 128, at[5] + 160)
+        calls.append((args, buf, s))
+    torch.cuda.synchronize()
+
+    def work(args, s):
+        torch.cuda.set_device(DEV)
+        for _ in range(4000):
+            st = lib.csa2p_page_plan(args, None, s.cuda_stream)
+            if st:
+                bad.append(st)
+
+    threads = [threading.Thread(target=work, args=(a, s)) for a, _, s in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
 
 
 # ------------------------------------------------------------------ offsets of the queries
