@@ -15,8 +15,8 @@ inline csa2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA2_OK 
 inline cudaStream_t as_stream(csa2_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool pow2_page(int32_t p) { return p >= 1 && p <= 65536 && (p & (p - 1)) == 0; }
 
-// false: not a valid rotation of rows of d channels
-bool rope_view(const csa2p_rope_axes *r, int32_t d, RopeView &v)
+// false: not a valid rotation of `rows` rows of d channels
+bool rope_view(const csa2p_rope_axes *r, int32_t d, int32_t rows, RopeView &v)
 {
     v = {nullptr, nullptr, 0, 0, 0, 0, 0};
     if (!r || r->rope_dim == 0) return true;
@@ -28,6 +28,7 @@ bool rope_view(const csa2p_rope_axes *r, int32_t d, RopeView &v)
         sum += r->section[k];
     }
     if (sum != r->rope_dim / 2) return false;
+    if (rows == 0) return true;                            // nothing is read: an empty tensor has no address
     if (!r->pos || !r->cos_sin || r->n_pos < 1 || !aligned(r->pos, 4) || !aligned(r->cos_sin, 4)) return false;
     v.pos = r->pos;
     v.cs = r->cos_sin;
@@ -77,7 +78,7 @@ csa2_status csa2p_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_
                        uint32_t *d_status, csa2_stream stream)
 {
     RopeView v;
-    if (rows < 0 || heads < 0 || d < 8 || d % 8 || d > (1 << 20) || !rope_view(rope, d, v)) return CSA2_ERR_INVALID_ARG;
+    if (rows < 0 || heads < 0 || d < 8 || d % 8 || d > (1 << 20) || !rope_view(rope, d, rows, v)) return CSA2_ERR_INVALID_ARG;
     if (rows == 0 || heads == 0) return CSA2_OK;
     if ((int64_t)heads * d > 0x7fffffff) return CSA2_ERR_INVALID_ARG;
     if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
@@ -92,7 +93,7 @@ csa2_status csa2p_write(const csa2p_cache *cache, const uint16_t *x, int64_t ldx
 {
     PagedView v;
     RopeView r;
-    if (!cache || !paged_view(*cache, v) || rows < 0 || !rope_view(rope, v.d, r)) return CSA2_ERR_INVALID_ARG;
+    if (!cache || !paged_view(*cache, v) || rows < 0 || !rope_view(rope, v.d, rows, r)) return CSA2_ERR_INVALID_ARG;
     if (rows == 0) return CSA2_OK;
     if (!x || !slot || !aligned(x, 16) || ldx % 8 || ldx < v.d) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_paged_write(v, x, ldx, rows, slot, r, d_status, as_stream(stream)));

@@ -161,6 +161,18 @@ def test_layer_with_more_rows_than_it_is_given():
     assert torch.equal(got[1].out, got[0].out[:6]) and torch.equal(got[1].lse, got[0].lse[:6])
 
 
+def test_layer_step_without_new_rows():
+    # drafts taken back and a request ended, nothing new: a step all the same
+    d, cs = 128, cos_sin(100, 32)
+    cache = paged.PagedCache.new(8, 16, d)
+    state = layers.PagedState(ints([0, 0]), ints([[-1] * 4] * 2), ints(range(8)), ints([8]))
+    for T, delta in ((50, [20, 30]), (0, [-5, -30]), (1, [1, 0])):
+        x, q, st = torch.randn((T, d), device=DEV).bfloat16(), torch.randn((T, 4, d), device=DEV).bfloat16(), status()
+        r = layers.paged_layer(cache, state, layers.PagedInput(q, x, ints(delta), cs), d_v=d, d_status=st)
+        assert r.out.shape == (T, 4, d) and int(st) == 0 and bool(torch.isfinite(r.out).all())
+    assert state.lens.tolist() == [16, 0] and int(state.n_free) == 7
+
+
 # ------------------------------------------------------------------ rows that no query sees
 @pytest.mark.parametrize("H,page,start,pos0,ratio", [
     (1, 16, 100, None, 1), (16, 1, 101, None, 1), (64, 1, 37, [0], 1), (3, 4, 60, [5], 1), (2, 8, 90, [0], 2), (1, 16, 1000, None, 1)])
