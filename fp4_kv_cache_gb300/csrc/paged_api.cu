@@ -40,6 +40,21 @@ bool rope_view(const csa2p_rope_axes *r, int32_t d, int32_t rows, RopeView &v)
     return true;
 }
 
+// Whether no two of the vectors of d elements at r * row + h * head share one (row, head >= d where
+// there are several).  Rows within heads, heads within rows: seen at once; else head by head.
+bool apart(int64_t row, int64_t head, int32_t rows, int32_t heads, int32_t d)
+{
+    if (rows < 2 || heads < 2) return true;
+    const __int128 R = row, H = head;
+    if (R >= H * (heads - 1) + d || H >= R * (rows - 1) + d) return true;
+    for (int64_t h = 1; h < heads; ++h) {
+        const __int128 at = H * h, r = at / R;
+        if (r >= rows) break;                              // and further off with every head
+        if ((r > 0 && at - r * R < d) || (r + 1 < rows && (r + 1) * R - at < d)) return false;
+    }
+    return true;
+}
+
 // 0: fine, else the status to return
 csa2_status attn_check(const csa2p_attn_args *a, PagedView &v)
 {
@@ -84,6 +99,7 @@ csa2_status csa2p_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_
     if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
     if (x_row % 8 || x_head % 8 || out_row % 8 || out_head % 8) return CSA2_ERR_INVALID_ARG;
     if (x_row < 0 || x_head < 0 || (heads > 1 && out_head < d) || (rows > 1 && out_row < d)) return CSA2_ERR_INVALID_ARG;
+    if (!apart(out_row, out_head, rows, heads, d)) return CSA2_ERR_INVALID_ARG;
     if (out == x && (x_row != out_row || x_head != out_head)) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_paged_rope(x, x_row, x_head, out, out_row, out_head, rows, heads, d, v, d_status, as_stream(stream)));
 }

@@ -124,7 +124,7 @@ typedef struct {
 /* csa2p_rope: x and out bf16 [rows, heads, d] with row and head strides in elements (multiples */
 /* of 8, both 16-byte aligned); out = the rotated x, each value rounded to bf16 once.  out may   */
 /* be x (with x's strides: only the turned channels are then touched); otherwise they must not   */
-/* overlap.  d % 8 == 0.                                                                          */
+/* overlap, and out's own vectors never.  d % 8 == 0.                                             */
 CSA2_API csa2_status csa2p_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_t *out, int64_t out_row,
                                 int64_t out_head, int32_t rows, int32_t heads, int32_t d,
                                 const csa2p_rope_axes *rope, uint32_t *d_status, csa2_stream stream);

@@ -9,6 +9,7 @@ import torch
 
 from fp4_kv_cache_gb300 import csa2, layers, paged
 from test_gpu_paged import AttnCase, DEV, FMTS, I32, check, close, cos_sin, ints, status, turned32, values64
+from test_paged_refusals import strides
 
 pytestmark = pytest.mark.gpu
 
@@ -102,6 +103,21 @@ def test_plans_of_two_sizes_at_once():
         t.join()
     torch.cuda.synchronize()
     assert not bad
+
+
+# ------------------------------------------------------------------ rotation
+def test_rope_strides_apart():
+    # every layout whose vectors lie apart, heads between rows and rows between heads among them
+    cs, n = cos_sin(50, 16), 0
+    for rows, heads, R, H in strides(False):
+        x, pos = torch.randn((rows, heads, 16), device=DEV).bfloat16(), torch.arange(rows, device=DEV, dtype=I32)
+        out = torch.full((1000,), 5.0, device=DEV).bfloat16().as_strided((rows, heads, 16), (R, H, 1))
+        want = turned32(x.float(), pos[None], cs, [8]).bfloat16()
+        assert torch.equal(paged.rope_axes(x, pos, cs, out=out), want), (rows, heads, R, H)
+        out.copy_(x)
+        assert torch.equal(paged.rope_axes(out, pos, cs, out=out), want), (rows, heads, R, H)
+        n += 1
+    assert n > 100
 
 
 # ------------------------------------------------------------------ offsets of the queries

@@ -36,3 +36,35 @@ def test_no_rows_have_no_positions(lib):
     bad = ctypes.byref(rope(sec=(31, 0, 0)))                               # still no rotation of 32 pairs
     assert lib.csa2p_write(c, None, 576, 0, None, bad, None, None) == INVALID
     assert lib.csa2p_rope(None, 1152, 576, None, 1152, 576, 0, 2, 576, bad, None, None) == INVALID
+
+
+# ------------------------------------------------------------------ outputs that overlap
+def test_rope_outputs_that_overlap_refused(lib):
+    # each stride holds a vector, and still the second head of a row lies on the next row
+    f, r, other = lib.csa2p_rope, ctypes.byref(rope()), FAKE + (1 << 30)
+    call = lambda rows, heads, row, head, x=FAKE: f(x, row, head, other, row, head, rows, heads, 576, r, None, None)  # noqa: E731
+    assert call(4, 2, 576, 576) == INVALID
+    assert call(4, 2, 576, 576, other) == INVALID                          # in place
+    assert call(4, 3, 1152, 576) == INVALID                                # heads reach the next row
+    assert call(4, 2, 576, 4 * 576 - 8) == INVALID                         # rows reach the next head
+    assert call(4, 2, 640, 960) == INVALID                                 # head 1 between two rows, on both
+    assert call(3, 3, 1 << 60, (1 << 60) + 8) == INVALID                   # far apart, but two by two on each other
+
+
+def strides(overlapping):
+    """(rows, heads, row stride, head stride) of vectors of 16 elements that share elements, or do not."""
+    for rows, heads in ((2, 2), (3, 2), (2, 4), (4, 3)):
+        for R in range(16, 120, 8):
+            for H in range(16, 120, 8):
+                at = sorted(r * R + h * H for r in range(rows) for h in range(heads))
+                if any(b - a < 16 for a, b in zip(at, at[1:])) == overlapping:
+                    yield rows, heads, R, H
+
+
+def test_rope_overlaps_by_enumeration(lib):
+    # (the other strides are accepted, and so run on a GPU only)
+    r, n = ctypes.byref(rope(dim=16, sec=(8, 0, 0))), 0
+    for rows, heads, R, H in strides(True):
+        assert lib.csa2p_rope(FAKE, R, H, FAKE + (1 << 20), R, H, rows, heads, 16, r, None, None) == INVALID, (rows, heads, R, H)
+        n += 1
+    assert n > 100
