@@ -11,6 +11,9 @@ using namespace csa2;
 namespace {
 
 inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+// Addresses of 4-byte values, NULL among them.
+template <typename... P>
+inline bool words(const P *...p) { return (aligned(p, 4) && ...); }
 inline csa2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
 inline cudaStream_t as_stream(csa2_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool pow2_page(int32_t p) { return p >= 1 && p <= 65536 && (p & (p - 1)) == 0; }
@@ -70,6 +73,7 @@ csa2_status attn_check(const csa2p_attn_args *a, PagedView &v)
     if (a->batch == 0 || a->n_tokens == 0) return CSA2_OK;
     if ((int64_t)a->n_tokens * a->n_heads > 0x7fffffff - 128) return CSA2_ERR_INVALID_ARG;
     if (!a->q || !aligned(a->q, 16) || !a->lens || !a->cu || (a->width > 0 && !a->block_table)) return CSA2_ERR_INVALID_ARG;
+    if (!words(a->block_table, a->lens, a->cu, a->pos0, a->kv_start)) return CSA2_ERR_INVALID_ARG;
     if (!a->pos0 && a->ratio_m != 1) return CSA2_ERR_INVALID_ARG;
     return CSA2_OK;
 }
@@ -85,6 +89,8 @@ csa2_status csa2p_page_plan(const csa2p_plan_args *a, uint32_t *d_status, csa2_s
     if (!a->n_free || !a->n_free_out || !a->cu) return CSA2_ERR_INVALID_ARG;
     if (a->batch > 0 && (!a->lens || !a->delta || !a->lens_out || !a->block_table)) return CSA2_ERR_INVALID_ARG;
     if ((a->free_cap > 0 && !a->free_pages) || (a->n_rows > 0 && !a->slot)) return CSA2_ERR_INVALID_ARG;
+    if (!words(a->lens, a->delta, a->lens_out, a->block_table, a->free_pages, a->n_free, a->n_free_out, a->cu, a->slot,
+               a->row_req, a->row_pos, d_status)) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_page_plan(*a, d_status, as_stream(stream)));
 }
 
@@ -96,7 +102,7 @@ csa2_status csa2p_rope(const uint16_t *x, int64_t x_row, int64_t x_head, uint16_
     if (rows < 0 || heads < 0 || d < 8 || d % 8 || d > (1 << 20) || !rope_view(rope, d, rows, v)) return CSA2_ERR_INVALID_ARG;
     if (rows == 0 || heads == 0) return CSA2_OK;
     if ((int64_t)heads * d > 0x7fffffff) return CSA2_ERR_INVALID_ARG;
-    if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
+    if (!x || !out || !aligned(x, 16) || !aligned(out, 16) || !words(d_status)) return CSA2_ERR_INVALID_ARG;
     if (x_row % 8 || x_head % 8 || out_row % 8 || out_head % 8) return CSA2_ERR_INVALID_ARG;
     if (x_row < 0 || x_head < 0 || (heads > 1 && out_head < d) || (rows > 1 && out_row < d)) return CSA2_ERR_INVALID_ARG;
     if (!apart(out_row, out_head, rows, heads, d)) return CSA2_ERR_INVALID_ARG;
@@ -111,7 +117,7 @@ csa2_status csa2p_write(const csa2p_cache *cache, const uint16_t *x, int64_t ldx
     RopeView r;
     if (!cache || !paged_view(*cache, v) || rows < 0 || !rope_view(rope, v.d, rows, r)) return CSA2_ERR_INVALID_ARG;
     if (rows == 0) return CSA2_OK;
-    if (!x || !slot || !aligned(x, 16) || ldx % 8 || ldx < v.d) return CSA2_ERR_INVALID_ARG;
+    if (!x || !slot || !words(slot, d_status) || !aligned(x, 16) || ldx % 8 || ldx < v.d) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_paged_write(v, x, ldx, rows, slot, r, d_status, as_stream(stream)));
 }
 
@@ -121,7 +127,7 @@ csa2_status csa2p_read(const csa2p_cache *cache, const int32_t *slot, int32_t ro
     PagedView v;
     if (!cache || !paged_view(*cache, v) || rows < 0) return CSA2_ERR_INVALID_ARG;
     if (rows == 0) return CSA2_OK;
-    if (!out || !slot || !aligned(out, 16) || ldo % 8 || ldo < v.d) return CSA2_ERR_INVALID_ARG;
+    if (!out || !slot || !words(slot, d_status) || !aligned(out, 16) || ldo % 8 || ldo < v.d) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_paged_read(v, slot, rows, out, ldo, d_status, as_stream(stream)));
 }
 
@@ -139,7 +145,7 @@ csa2_status csa2p_attn(const csa2p_attn_args *a, uint16_t *out, float *lse, void
     const csa2_status st = attn_check(a, v);
     if (st != CSA2_OK) return st;
     if (a->batch == 0 || a->n_tokens == 0) return CSA2_OK;
-    if (!out || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
+    if (!out || !aligned(out, 16) || !words(lse, d_status)) return CSA2_ERR_INVALID_ARG;
     const size_t need = paged_attn_ws_bytes(*a);
     if (ws_bytes < need) return CSA2_ERR_WORKSPACE;
     if (need && (!ws || !aligned(ws, 16))) return CSA2_ERR_INVALID_ARG;

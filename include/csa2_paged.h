@@ -22,7 +22,8 @@
  * input, and lets its dependents start their set-up right after that.  Calls on different
  * streams may run concurrently while their outputs and workspaces are disjoint; two captured
  * graphs that may run at the same time need workspaces of their own.  The calls work on the
- * current device, which has to be the one that holds the pointers.
+ * current device, which has to be the one that holds the pointers.  Addresses of 32-bit values
+ * are multiples of 4 (else INVALID_ARG, as with the alignments given below).
  */
 #ifndef CSA2_PAGED_H
 #define CSA2_PAGED_H

@@ -68,3 +68,31 @@ def test_rope_overlaps_by_enumeration(lib):
         assert lib.csa2p_rope(FAKE, R, H, FAKE + (1 << 20), R, H, rows, heads, 16, r, None, None) == INVALID, (rows, heads, R, H)
         n += 1
     assert n > 100
+
+
+# ------------------------------------------------------------------ addresses that hold no 32-bit values
+OFF = FAKE + 2
+
+
+@pytest.mark.parametrize("name", ["lens", "delta", "lens_out", "block_table", "free_pages", "n_free", "n_free_out", "cu",
+                                  "slot", "row_req", "row_pos"])
+def test_plan_addresses_refused(lib, name):
+    assert lib.csa2p_page_plan(plan(**{name: OFF}), None, None) == INVALID
+
+
+@pytest.mark.parametrize("name", ["block_table", "lens", "cu", "pos0", "kv_start"])
+def test_attn_addresses_refused(lib, name):
+    assert lib.csa2p_attn(ctypes.byref(attn(**{name: OFF})), FAKE, FAKE, FAKE, 1 << 40, None, None) == INVALID
+
+
+def test_other_addresses_refused(lib):
+    c, r, other = ctypes.byref(cache()), ctypes.byref(rope()), FAKE + (1 << 20)
+    assert lib.csa2p_write(c, FAKE, 576, 4, OFF, None, None, None) == INVALID
+    assert lib.csa2p_read(c, OFF, 4, FAKE, 576, None, None) == INVALID
+    assert lib.csa2p_attn(ctypes.byref(attn()), FAKE, OFF, FAKE, 1 << 40, None, None) == INVALID
+    for status in (OFF, FAKE + 1):
+        assert lib.csa2p_page_plan(plan(), status, None) == INVALID
+        assert lib.csa2p_rope(FAKE, 576, 576, other, 576, 576, 4, 1, 576, r, status, None) == INVALID
+        assert lib.csa2p_write(c, FAKE, 576, 4, FAKE, None, status, None) == INVALID
+        assert lib.csa2p_read(c, FAKE, 4, FAKE, 576, status, None) == INVALID
+        assert lib.csa2p_attn(ctypes.byref(attn()), FAKE, FAKE, FAKE, 1 << 40, status, None) == INVALID
