@@ -204,8 +204,8 @@ def page_plan(lens, delta, block_table, free_pages, n_free, page: int, n_rows: i
               plan: Optional[PagePlan] = None, d_status=None, stream=None) -> PagePlan:
     """One step of the requests' bookkeeping: block_table [batch, width] and free_pages are updated,
     the rest is returned (into `plan`'s tensors when given).  in_place: lens and n_free are
-    overwritten with the new lengths and the new count, as a captured graph needs it.  See
-    csa2p_page_plan."""
+    overwritten with the new lengths and the new count, as a captured graph needs it (a plan given
+    with it holds these two tensors).  See csa2p_page_plan."""
     dev, B = lens.get_device(), lens.shape[0]
     width = block_table.shape[1]
     if plan is None:
@@ -225,6 +225,8 @@ def page_plan(lens, delta, block_table, free_pages, n_free, page: int, n_rows: i
         at_len, at_n = _need(plan.lens, "plan.lens", _i32, B, dev), _need(plan.n_free, "plan.n_free", _i32, 1, dev)
         at_cu, at_slot = _need(plan.cu, "plan.cu", _i32, B + 1, dev), _need(plan.slot, "plan.slot", _i32, n_rows, dev)
         at_req, at_pos = _need(plan.row_req, "plan.row_req", _i32, n_rows, dev), _need(plan.row_pos, "plan.row_pos", _i32, n_rows, dev)
+        if in_place and (at_len != lens.data_ptr() or at_n != n_free.data_ptr()):
+            raise ValueError("in_place: plan.lens and plan.n_free must be lens and n_free")
     a = _PLAN.pack(B, page, width, free_pages.shape[0], n_rows, _need(lens, "lens", _i32, B, dev),
                    _need(delta, "delta", _i32, B, dev), at_len, _need(block_table, "block_table", _i32, B * width, dev),
                    _need(free_pages, "free_pages", _i32, None, dev), _need(n_free, "n_free", _i32, 1, dev), at_n, at_cu, at_slot,

@@ -78,6 +78,20 @@ def test_plan_steps_with_shortages(B, page, n_pages, most, n_rows, seed, in_plac
     run_plan(steps, [0] * B, [[-1] * width for _ in range(B)], list(range(n_pages)), n_pages, page, n_rows, in_place)
 
 
+def test_plan_in_place_into_a_plan():
+    # in_place overwrites lens and n_free: a plan with others is refused, nothing is done
+    table, free, lens, n = ints([[-1] * 4] * 2), ints(range(8)), ints([0, 0]), ints([8])
+    first = paged.page_plan(lens, ints([5, 0]), table, free, n, 4, 6, in_place=True)
+    assert first.lens is lens and first.n_free is n
+    other = paged.page_plan(lens, ints([0, 0]), table, free, n, 4, 6)
+    for p in (other, paged.PagePlan(lens, other.cu, other.slot, other.row_req, other.row_pos, other.n_free)):
+        with pytest.raises(ValueError, match="in_place"):
+            paged.page_plan(lens, ints([1, 9]), table, free, n, 4, 6, in_place=True, plan=p)
+    assert lens.tolist() == [5, 0] and int(n) == 6
+    assert paged.page_plan(lens, ints([1, 2]), table, free, n, 4, 6, in_place=True, plan=first) is first
+    assert lens.tolist() == [6, 2] and int(n) == 5 and first.slot.tolist()[:3] == [6 * 4 + 1, 5 * 4, 5 * 4 + 1]
+
+
 def test_plans_of_two_sizes_at_once():
     # two host threads, each with its own stream: the larger plan's shared memory is not taken away
     lib, calls, bad = paged._lib(), [], []
