@@ -69,7 +69,8 @@ csa2_status attn_check(const csa2p_attn_args *a, PagedView &v)
     // the kernel tells rows by 32-bit offsets: codes in 16 bytes, scales in bytes
     if (v.code_page * v.n_pages >= (int64_t(1) << 36) || v.scale_page * v.n_pages >= (int64_t(1) << 32)) return CSA2_ERR_UNSUPPORTED;
     if (a->width < 0 || a->window < 0 || a->ratio_m < 1) return CSA2_ERR_INVALID_ARG;
-    if (!(a->sm_scale > 0.0f) || a->sm_scale > 3.0e38f) return CSA2_ERR_INVALID_ARG;
+    // the kernel takes logits to base 2: the scale times log2(e) has to be a float
+    if (!(a->sm_scale > 0.0f) || a->sm_scale > 2.3e38f) return CSA2_ERR_INVALID_ARG;
     if (a->batch == 0 || a->n_tokens == 0) return CSA2_OK;
     if ((int64_t)a->n_tokens * a->n_heads > 0x7fffffff - 128) return CSA2_ERR_INVALID_ARG;
     if (!a->q || !aligned(a->q, 16) || !a->lens || !a->cu || (a->width > 0 && !a->block_table)) return CSA2_ERR_INVALID_ARG;

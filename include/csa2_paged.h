@@ -178,7 +178,7 @@ typedef struct {
     int32_t width;            /* block table entries a request                                   */
     int32_t window;           /* >= 0; 0: no window                                              */
     int32_t ratio_m;          /* tokens an entry stands for, >= 1                                */
-    float sm_scale;
+    float sm_scale;           /* above 0, at most 2.3e38                                         */
     const uint16_t *q;        /* bf16 [n_tokens, n_heads, d_qk], 16-byte aligned                 */
     const int32_t *block_table; /* [batch, width]                                                */
     const int32_t *lens;      /* [batch] rows held, the new tokens' included                     */

@@ -96,3 +96,10 @@ def test_other_addresses_refused(lib):
         assert lib.csa2p_write(c, FAKE, 576, 4, FAKE, None, status, None) == INVALID
         assert lib.csa2p_read(c, FAKE, 4, FAKE, 576, status, None) == INVALID
         assert lib.csa2p_attn(ctypes.byref(attn()), FAKE, FAKE, FAKE, 1 << 40, status, None) == INVALID
+
+
+# ------------------------------------------------------------------ logit scales
+@pytest.mark.parametrize("scale", [2.4e38, 2.9e38, -1.0])
+def test_attn_scales_refused(lib, scale):
+    # times log2(e) no float is left: 0 x infinity would make NaN of a logit of 0
+    assert lib.csa2p_attn(ctypes.byref(attn(sm_scale=scale)), FAKE, FAKE, FAKE, 1 << 40, None, None) == INVALID
