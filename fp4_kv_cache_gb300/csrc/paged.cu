@@ -460,9 +460,10 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8])
 
 // A thread takes pieces of eight channels (16 bytes) of one row of q; blockIdx.x = row, the
 // row's pieces are shared by gridDim.y blocks.  In place (`same`) only the pieces that hold
-// turned channels are visited.  HBM bounds it: 604 MB of three-axis rows out of place take 104 us,
+// turned channels are visited; x and out are then the same memory, which a thread reads before it writes
+// it, so neither is __restrict__.  HBM bounds it: 604 MB of three-axis rows out of place take 104 us,
 // 5.8 TB/s; 32 x 64 rows (4.7 MB, from L2) take 2 us.
-__global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *__restrict__ x, int64_t x_row, int64_t x_head,
+__global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *x, int64_t x_row, int64_t x_head,
                                                          uint16_t *out, int64_t out_row, int64_t out_head, int32_t heads,
                                                          int32_t d, int32_t first_piece, int64_t rows,
                                                          const __grid_constant__ RopeView R,
