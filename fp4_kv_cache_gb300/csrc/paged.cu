@@ -494,6 +494,9 @@ __global__ void __launch_bounds__(256) paged_rope_kernel(const uint16_t *x, int6
 }
 
 // ---------------------------------------------------------------- write
+// Inputs here are not `const __restrict__`: these kernels begin while the one before them may still be
+// writing x and the slots (they wait for it first), so that the memory is not read-only for as long as
+// they run, which the loads of such pointers take for granted.
 __device__ __forceinline__ float max_nan(float a, float b)      // NaN if either is
 {
     float d;
@@ -508,8 +511,8 @@ __device__ __forceinline__ float max_nan(float a, float b)      // NaN if either
 // 16,384 rows take 12.1 us (19 MB in, 5 MB out), 32 rows 2.6 us.
 // ROPE 0: none; 1: RopeView.quads; 2: any.
 template <int FMT, int ROPE>
-__global__ void __launch_bounds__(1024) paged_write_kernel(const PagedView C, const uint16_t *__restrict__ x, int64_t ldx,
-                                                           int32_t rows, const int32_t *__restrict__ slot,
+__global__ void __launch_bounds__(1024) paged_write_kernel(const PagedView C, const uint16_t *x, int64_t ldx,
+                                                           int32_t rows, const int32_t *slot,
                                                            const __grid_constant__ RopeView R, uint32_t *d_status)
 {
     pdl_wait();
@@ -623,8 +626,8 @@ __device__ __noinline__ void read_slow(Raw<FMT, 2> r, uint16_t *to)
 // first is decoded, because the slot, the row and the store are one chain of latencies.  16,384 rows
 // of 576 (5 MB in, 19 MB out) take 7.8 us, 32 rows 1.6 us.
 template <int FMT, int U>
-__global__ void __launch_bounds__(1024) paged_read_kernel(const PagedView C, const int32_t *__restrict__ slot, int32_t rows,
-                                                         uint16_t *__restrict__ out, int64_t ldo, uint32_t f0, uint32_t f4,
+__global__ void __launch_bounds__(1024) paged_read_kernel(const PagedView C, const int32_t *slot, int32_t rows,
+                                                         uint16_t *out, int64_t ldo, uint32_t f0, uint32_t f4,
                                                          uint32_t *d_status)
 {
     pdl_wait();
