@@ -28,7 +28,8 @@ MAX_BATCH = 16384
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _i32, _bf16, _f32 = torch.int32, torch.bfloat16, torch.float32
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (a torch without CUDA has neither; nothing there gets as far as a stream)
+_raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 class CacheArgs(ctypes.Structure):

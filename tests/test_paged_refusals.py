@@ -1,11 +1,14 @@
 """Paged-cache calls that are refused on the host, or answered there: nothing here reaches the GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from fp4_kv_cache_gb300 import paged
-from test_paged_host import FAKE, INVALID, attn, cache, lib, plan, rope      # noqa: F401
+from test_paged_host import FAKE, INVALID, ROOT, attn, cache, lib, plan, rope      # noqa: F401
 
 U8 = torch.uint8
 
@@ -103,3 +106,15 @@ def test_other_addresses_refused(lib):
 def test_attn_scales_refused(lib, scale):
     # times log2(e) no float is left: 0 x infinity would make NaN of a logit of 0
     assert lib.csa2p_attn(ctypes.byref(attn(sm_scale=scale)), FAKE, FAKE, FAKE, 1 << 40, None, None) == INVALID
+
+
+# ------------------------------------------------------------------ a torch without CUDA
+def test_package_imports_without_cuda():
+    # layers and paged can be imported, and a cache on the CPU be made, where torch has no CUDA calls
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from fp4_kv_cache_gb300 import layers, paged\n"
+            "paged.PagedCache.new(2, 16, 64, device='cpu')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=dict(os.environ, PYTHONPATH=ROOT), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
