@@ -186,8 +186,10 @@ typedef struct {
     const int32_t *pos0;      /* [batch] or NULL                                                 */
     const int32_t *kv_start;  /* [batch] or NULL                                                 */
 } csa2p_attn_args;
-/* Workspace: parts of rows whose keys are split over the GPU.  Its size depends on the arguments' */
-/* shapes and on the current device; its contents need no preparation.                            */
+/* Workspace: parts of rows whose keys are split over the GPU.  Its size depends on d_v and on the  */
+/* current device; its contents need no preparation.  The size is 0 for a call that csa2p_attn     */
+/* would refuse or that has nothing to do, pointers that are NULL or misaligned included: to size a */
+/* workspace before the tensors exist, give any aligned addresses in their place (nothing is read). */
 CSA2_API size_t csa2p_attn_workspace_size(const csa2p_attn_args *a);
 CSA2_API csa2_status csa2p_attn(const csa2p_attn_args *a, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
                                 uint32_t *d_status, csa2_stream stream);
