@@ -229,3 +229,217 @@ def test_attn_rows_past_the_table_that_none_sees(lens, pos0, window, start, flag
     assert int(st) == (csa2.DEV_BAD_INDEX if flagged else 0)
     empty = torch.tensor([r.start >= min(r.stop, 304) for r in seen], device=DEV)
     assert torch.equal((lse == -math.inf).all(1), empty) and bool((out[empty] == 0).all())
+
+
+# ------------------------------------------------------------------ values that are not finite, scales far out
+def same(got, want):
+    """Equal bits, or NaN on both sides."""
+    nan = torch.isnan(want)
+    return torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("d", [32, 576])
+@pytest.mark.parametrize("fmt", [paged.MXFP4, paged.NVFP4_E4M3_16, paged.MXFP8])
+def test_read_every_scale_byte(fmt, d):
+    # row r has scale byte r (and its neighbour in the next block) under random codes, NaN codes among them
+    g = torch.Generator(device=DEV).manual_seed(fmt)
+    c = paged.PagedCache.new(32, 8, d, fmt)
+    c.codes.copy_(torch.randint(0, 256, c.codes.shape, generator=g, device=DEV))
+    byte = torch.arange(256, device=DEV).view(32, 8, 1) + torch.arange(c.scales.shape[2], device=DEV) % 2
+    c.scales.copy_(byte % 256)
+    st = status()
+    out = paged.paged_read(c, ints(range(256)), d_status=st)
+    assert same(out, values64(c.codes.flatten(0, 1), c.scales.flatten(0, 1), fmt).bfloat16()) and int(st) == 0
+
+
+def test_read_bf16_as_it_is():
+    c = paged.PagedCache.new(65536 // 64, 2, 32, paged.BF16)
+    bits = torch.arange(65536, device=DEV, dtype=I32).to(torch.int16)
+    c.codes.view(torch.int16).copy_(bits.view(c.codes.shape))
+    out = paged.paged_read(c, ints(range(2048)))
+    assert torch.equal(out.view(torch.int16).flatten(), bits)
+
+
+@pytest.mark.parametrize("fmt", [paged.MXFP4, paged.NVFP4_E4M3_16, paged.MXFP8])
+@pytest.mark.parametrize("rope", [0, 64])
+def test_write_blocks_not_finite(fmt, rope):
+    # the block itself, not only those beside it, as the contiguous codecs write it
+    g = torch.Generator(device=DEV).manual_seed(fmt + rope)
+    x = torch.randn((64, 576), generator=g, device=DEV).bfloat16()
+    for r, (col, v) in enumerate([(5, math.inf), (5, -math.inf), (40, math.nan), (511, math.inf), (100, math.nan)]):
+        x[r, col] = v
+    x[5, 64:96], x[6, 96:112], x[7, :] = math.nan, math.inf, -math.inf
+    x[8, 3], x[8, 4] = math.nan, math.inf
+    if rope:
+        x[9, 520], x[10, 575], x[11, 544:] = math.inf, math.nan, -math.inf
+    cs, pos = cos_sin(64, rope) if rope else None, torch.arange(64, device=DEV, dtype=I32)
+    c, st = paged.PagedCache.new(4, 16, 576, fmt), status()
+    paged.paged_write(c, x, ints(range(64)), *((pos, cs) if rope else ()), d_status=st)
+    assert int(st) == csa2.DEV_NONFINITE
+    if fmt == paged.MXFP8:
+        codes, scales = csa2.quant_fp8(turned32(x.float(), pos[None], cs, [32]) if rope else x)
+    elif rope:
+        codes, scales = torch.empty_like(c.codes.view(64, -1)), torch.empty_like(c.scales.view(64, -1))
+        csa2.csa2_rope_quant_fp4([(x, codes, scales, 64, pos, cs, fmt)])
+    else:
+        codes, scales = csa2.quant_fp4(x, fmt=fmt)
+    assert torch.equal(c.codes.view(64, -1), codes) and torch.equal(c.scales.view(64, -1), scales)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("channels", [[3], [300], [512], [575], [530, 40], [545]])
+def test_attn_not_finite_channels(fmt, channels):
+    # in rows of 576: each part of a row's staging marks its key, in every tile, for the queries that see it
+    c = AttnCase([300, 140, 513], [5, 40, 1], 16, 576, 512, fmt, 16, seed=26)
+    for b, j in ((0, 299), (0, 300), (1, 120), (1, 139), (2, 513)):        # 300 and 513 lie past the rows held
+        pg, off = int(c.table[b, j // 16]), j % 16
+        for ch in channels:
+            if fmt == paged.BF16:
+                c.cache.codes[pg, off, ch] = math.nan if j % 2 else -math.inf
+            elif fmt == paged.MXFP8 and j % 2:
+                c.cache.codes[pg, off, ch] = 0x7F
+            else:
+                c.cache.scales[pg, off, ch // (16 if fmt == paged.NVFP4_E4M3_16 else 32)] = 0xFF
+    out, _ = check(c)
+    assert int(torch.isnan(out).any(-1).any(-1).sum()) == 1 + 20
+
+
+# ------------------------------------------------------------------ many requests, far slots
+def test_attn_most_requests():
+    # 16,384 requests, most without a token: as a call of those that have some
+    B, H, d = paged.MAX_BATCH, 2, 64
+    r = np.random.default_rng(7)
+    new = np.where(r.random(B) < 0.03, r.integers(1, 4, B), 0)
+    new[[0, B - 1]] = 2
+    lens = new + r.integers(0, 90, B)
+    some = new > 0
+    table = r.integers(0, 50, (B, 6))
+    cache = paged.PagedCache.new(50, 16, d, paged.MXFP8)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    cache.codes.copy_(torch.randint(0, 0x78, cache.codes.shape, generator=g, device=DEV))
+    cache.scales.fill_(120)
+    q = torch.randn((int(new.sum()), H, d), generator=g, device=DEV).bfloat16()
+    got = []
+    for keep in (np.ones(B, bool), some):
+        cu, st = np.concatenate([[0], np.cumsum(new[keep])]), status()
+        got.append(paged.paged_attn(q, cache, ints(table[keep]), ints(lens[keep]), ints(cu), d_status=st))
+        assert int(st) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_plan_most_requests():
+    B, page = paged.MAX_BATCH, 4
+    r = np.random.default_rng(9)
+    steps = [r.integers(0, 9, B), np.where(r.random(B) < 0.5, -r.integers(0, 9, B), 1), np.full(B, -9)]
+    lens, run = np.zeros(B, int), []
+    for d in steps:
+        run.append([int(v) for v in np.maximum(d, -lens)])
+        lens = lens + run[-1]
+    run_plan(run, [0] * B, [[-1] * 4 for _ in range(B)], list(range(20000)), 20000, page, 80000, True)
+
+
+@pytest.mark.parametrize("fmt", [paged.BF16, paged.MXFP8])
+def test_write_and_read_far_slots(fmt):
+    # rows whose byte offsets pass 32 bits
+    page, d = 64, 576
+    n = (5 << 30) // (page * d * (2 if fmt == paged.BF16 else 1))
+    shape = (n, page, d)
+    codes = torch.empty(shape, dtype=torch.bfloat16 if fmt == paged.BF16 else torch.uint8, device=DEV)
+    c = paged.PagedCache(codes, None if fmt == paged.BF16 else torch.empty((n, page, d // 32), dtype=torch.uint8, device=DEV))
+    x = torch.randn((100, d), device=DEV).bfloat16()
+    slot = torch.cat([torch.arange(50, device=DEV), n * page - 1 - torch.arange(50, device=DEV)]).to(I32)
+    paged.paged_write(c, x, slot)
+    out = paged.paged_read(c, slot)
+    if fmt == paged.BF16:
+        assert torch.equal(out, x) and torch.equal(codes.view(-1, d)[slot.long()], x)
+    else:
+        want, scales = csa2.quant_fp8(x)
+        assert torch.equal(codes.view(-1, d)[slot.long()], want)
+        assert torch.equal(out, values64(want, scales, fmt).bfloat16())
+
+
+# ------------------------------------------------------------------ together
+def test_further_layers_of_a_step():
+    # two layers of one step share the plan: the second as if it had been first, on its own cache and input
+    H, d, fmt = 8, 128, paged.NVFP4_E4M3_16
+    g, cs = torch.Generator(device=DEV).manual_seed(27), cos_sin(200, 32)
+    new_state = lambda: layers.PagedState(ints([0, 0, 0]), ints([[-1] * 8] * 3), ints(range(20)), ints([20]))  # noqa: E731
+    shared, alone = new_state(), new_state()
+    caches = [paged.PagedCache.new(20, 16, d, fmt) for _ in range(3)]
+    for delta in ([40, 1, 0], [1, 1, 30], [1, -1, 1]):
+        T = sum(max(v, 0) for v in delta) + 2
+        xs = [layers.PagedInput(torch.randn((T, H, d), generator=g, device=DEV).bfloat16(),
+                                torch.randn((T, d), generator=g, device=DEV).bfloat16(), ints(delta), cs) for _ in range(2)]
+        st, n = status(), T - 2
+        first = layers.paged_layer(caches[0], shared, xs[0], d_v=d, d_status=st)
+        again = layers.paged_layer_again(caches[1], shared, xs[1], first.plan, window=20, d_v=d, d_status=st)
+        want = layers.paged_layer(caches[2], alone, xs[1], window=20, d_v=d, d_status=st)
+        assert int(st) == 0 and again.plan is first.plan
+        assert torch.equal(again.out[:n], want.out[:n]) and torch.equal(again.lse[:n], want.lse[:n])
+        assert torch.equal(caches[1].codes, caches[2].codes) and torch.equal(caches[1].scales, caches[2].scales)
+        assert not torch.equal(caches[0].codes, caches[1].codes)
+
+
+def test_layer_captured_and_replayed():
+    # one captured step of plan, rotation, write and attention, replayed with new rows, as the same steps made one by one
+    H, d, B, T = 16, 128, 5, 12
+    g, cs = torch.Generator(device=DEV).manual_seed(28), cos_sin(300, 32)
+    make = lambda: (paged.PagedCache.new(30, 16, d, paged.MXFP4),                              # noqa: E731
+                    layers.PagedState(ints([0] * B), ints([[-1] * 10] * B), ints(range(30)), ints([30])))
+    (cache, state), (cache2, state2) = make(), make()
+    x = layers.PagedInput(torch.zeros((T, H, d), device=DEV).bfloat16(), torch.zeros((T, d), device=DEV).bfloat16(), ints([0] * B), cs)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        layers.paged_layer(cache, state, x, d_v=d)                        # nothing new: only to have run once
+    torch.cuda.synchronize()
+    graph, st = torch.cuda.CUDAGraph(), status()
+    with torch.cuda.graph(graph):
+        r = layers.paged_layer(cache, state, x, d_v=d, d_status=st)
+    for delta in ([3, 0, 1, 7, 1], [1, 1, 1, 1, 1], [-2, 5, 0, -100, 4], [0, 0, 0, 0, 0], [1, 1, 1, 9, 0]):
+        x.q.normal_(generator=g), x.x.normal_(generator=g), x.delta.copy_(ints(delta))
+        graph.replay()
+        want = layers.paged_layer(cache2, state2, x, d_v=d)
+        n = sum(max(v, 0) for v in delta)
+        assert torch.equal(r.out[:n], want.out[:n]) and torch.equal(r.lse[:n], want.lse[:n])
+        for a, b in ((state.lens, state2.lens), (state.block_table, state2.block_table), (state.n_free, state2.n_free),
+                     (r.plan.slot, want.plan.slot), (cache.codes, cache2.codes), (cache.scales, cache2.scales)):
+            assert torch.equal(a, b)
+    assert int(st) == 0
+
+
+def test_calls_at_once_on_streams_and_in_graphs():
+    # long calls back to back on two streams, then two graphs with workspaces of their own replayed side by side
+    cs = [AttnCase([9000, 500], [40, 30], 64, 576, 512, paged.MXFP4, 64, seed=s) for s in (31, 32)]
+    args, want, outs, spaces = [], [], [], []
+    for c in cs:
+        want.append(c.run())
+        args.append((c.q, c.cache, torch.from_numpy(c.table).to(DEV).to(I32), ints(c.lens), ints(c.cu)))
+        outs.append([(torch.empty_like(want[-1][0]), torch.empty_like(want[-1][1])) for _ in range(6)])
+        spaces.append(torch.empty(1 << 27, dtype=torch.uint8, device=DEV))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def calls(i, stream=None):
+        for out, lse in outs[i]:
+            paged.paged_attn(*args[i], d_v=512, sm_scale=cs[i].sm, out=out, lse=lse, workspace=spaces[i], stream=stream)
+
+    def compare():
+        torch.cuda.synchronize()
+        for i in range(2):
+            for out, lse in outs[i]:
+                assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+                out.zero_(), lse.zero_()
+        torch.cuda.synchronize()
+
+    torch.cuda.synchronize()
+    for i in range(2):
+        calls(i, streams[i])
+    compare()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            calls(i)
+    for _ in range(2):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        compare()
