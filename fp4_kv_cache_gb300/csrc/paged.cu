@@ -622,61 +622,48 @@ __device__ __noinline__ void read_slow(Raw<FMT, 2> r, uint16_t *to)
     }
 }
 
-// Sixteen channels a thread, U rows at once: every row's code and scale are asked for before the
-// first is decoded, because the slot, the row and the store are one chain of latencies.  16,384 rows
-// of 576 (5 MB in, 19 MB out) take 7.8 us, 32 rows 1.6 us.
-template <int FMT, int U>
+// Sixteen channels of one row a thread.  Two rows a thread, both asked for before the first is
+// decoded, were slower at every size and coded format (16,384 rows of 576, MXFP4: 7.9 us; 131,072 rows,
+// MXFP8: 62 against 41 us) and 4% faster for large bf16 reads only.  16,384 rows (5 MB in, 19 MB out)
+// take 6.1 us, 32 rows 1.7 us; 524,288 rows 147 us, 5.2 TB/s.
+template <int FMT>
 __global__ void __launch_bounds__(1024) paged_read_kernel(const PagedView C, const int32_t *slot, int32_t rows,
-                                                         uint16_t *out, int64_t ldo, uint32_t f0, uint32_t f4,
-                                                         uint32_t *d_status)
+                                                          uint16_t *out, int64_t ldo, uint32_t f0, uint32_t f4,
+                                                          uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
     const int part = threadIdx.x;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y * U; r0 < rows; r0 += (int64_t)gridDim.x * blockDim.y * U) {
-        int32_t sls[U];
-        Raw<FMT, 2> raw[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int64_t r = r0 + k * blockDim.y + threadIdx.y;
-            sls[k] = r < rows ? slot[r] : -1;
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < rows; r0 += (int64_t)gridDim.x * blockDim.y) {
+        const int64_t r = r0 + threadIdx.y;
+        const int32_t sl = r < rows ? slot[r] : -1;
+        if (sl >= C.n_slots && part == 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        if (sl < 0 || sl >= C.n_slots) continue;
+        Raw<FMT, 2> raw;
+        load_raw(raw, C.codes + C.code_at(sl) + part * code_bytes<FMT>(16),
+                 C.scales + C.scale_at(sl) + (FMT == CSA2P_NVFP4_E4M3_16 ? part : part >> 1));
+        uint16_t *to = out + r * ldo + 16 * part;
+        if (FMT != CSA2P_BF16 && special(raw)) {
+            read_slow(raw, to);
+            continue;
         }
+        uint32_t v[8];
+        if (FMT == CSA2P_BF16) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (sls[k] >= C.n_slots) {
-                if (part == 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-                sls[k] = -1;
+            for (int i = 0; i < 8; ++i) v[i] = raw.w[i % Raw<FMT, 2>::kWords];
+        } else {
+            uint32_t p[8];
+            decode(raw, p, f0, f4);
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {              // channels 0 4, 1 5, 2 6, 3 7 into order
+                v[h] = prmt(p[h], p[h + 1], 0x5410u);
+                v[h + 1] = prmt(p[h + 2], p[h + 3], 0x5410u);
+                v[h + 2] = prmt(p[h], p[h + 1], 0x7632u);
+                v[h + 3] = prmt(p[h + 2], p[h + 3], 0x7632u);
             }
-            if (sls[k] >= 0)
-                load_raw(raw[k], C.codes + C.code_at(sls[k]) + part * code_bytes<FMT>(16),
-                         C.scales + C.scale_at(sls[k]) + (FMT == CSA2P_NVFP4_E4M3_16 ? part : part >> 1));
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (sls[k] < 0) continue;
-            uint16_t *to = out + (r0 + k * blockDim.y + threadIdx.y) * ldo + 16 * part;
-            if (FMT != CSA2P_BF16 && special(raw[k])) {
-                read_slow(raw[k], to);
-                continue;
-            }
-            uint32_t v[8];
-            if (FMT == CSA2P_BF16) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = raw[k].w[i % Raw<FMT, 2>::kWords];
-            } else {
-                uint32_t p[8];
-                decode(raw[k], p, f0, f4);
-#pragma unroll
-                for (int h = 0; h < 8; h += 4) {          // channels 0 4, 1 5, 2 6, 3 7 into order
-                    v[h] = prmt(p[h], p[h + 1], 0x5410u);
-                    v[h + 1] = prmt(p[h + 2], p[h + 3], 0x5410u);
-                    v[h + 2] = prmt(p[h], p[h + 1], 0x7632u);
-                    v[h + 3] = prmt(p[h + 2], p[h + 3], 0x7632u);
-                }
-            }
-            reinterpret_cast<uint4 *>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<uint4 *>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-        }
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 
@@ -775,18 +762,16 @@ cudaError_t launch_paged_write(const PagedView &v, const uint16_t *x, int64_t ld
 #define CSA2P_PICK(K, N) (v.fmt == CSA2P_MXFP4 ? K<CSA2P_MXFP4, N> : v.fmt == CSA2P_NVFP4_E4M3_16 ? K<CSA2P_NVFP4_E4M3_16, N> \
                           : v.fmt == CSA2P_MXFP8 ? K<CSA2P_MXFP8, N> : K<CSA2P_BF16, N>)
     auto k = rope.dim == 0 ? CSA2P_PICK(paged_write_kernel, 0) : rope.quads ? CSA2P_PICK(paged_write_kernel, 1) : CSA2P_PICK(paged_write_kernel, 2);
+#undef CSA2P_PICK
     return launch_pdl(k, dim3(row_grid(v.d, rows)), row_block(v.d), 0, s, 1, v, x, ldx, rows, slot, rope, d_status);
 }
 
 cudaError_t launch_paged_read(const PagedView &v, const int32_t *slot, int32_t rows, uint16_t *out, int64_t ldo,
                               uint32_t *d_status, cudaStream_t s)
 {
-    // one row a thread while there are few, two once they fill the GPU
-    const bool two = rows >= (int64_t)device_sm_count() * row_block(v.d).y * 2;
-    auto k = two ? CSA2P_PICK(paged_read_kernel, 2) : CSA2P_PICK(paged_read_kernel, 1);
-#undef CSA2P_PICK
-    return launch_pdl(k, dim3(row_grid(v.d, two ? (rows + 1) / 2 : rows)), row_block(v.d), 0, s, 1, v, slot, rows, out, ldo, kCodeAt0,
-                      kCodeAt4, d_status);
+    auto k = v.fmt == CSA2P_MXFP4 ? paged_read_kernel<CSA2P_MXFP4> : v.fmt == CSA2P_NVFP4_E4M3_16 ? paged_read_kernel<CSA2P_NVFP4_E4M3_16>
+             : v.fmt == CSA2P_MXFP8 ? paged_read_kernel<CSA2P_MXFP8> : paged_read_kernel<CSA2P_BF16>;
+    return launch_pdl(k, dim3(row_grid(v.d, rows)), row_block(v.d), 0, s, 1, v, slot, rows, out, ldo, kCodeAt0, kCodeAt4, d_status);
 }
 
 } // namespace csa2
