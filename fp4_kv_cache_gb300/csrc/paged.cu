@@ -505,11 +505,12 @@ __device__ __forceinline__ float max_nan(float a, float b)      // NaN if either
 }
 
 // Blocks of (d / 16, rows) threads: thread (x, y) takes sixteen channels of a row (32 bytes of x),
-// a scale block of 32 channels is two neighbours of one warp (d / 16 is even).  What bounds it is
-// its instructions, about as many for the addresses and the scale as for eight channels: with
-// eight channels a thread 16,384 rows of 576 took 9.7 us (MXFP4, no rotation).  With rotation
-// 16,384 rows take 12.1 us (19 MB in, 5 MB out), 32 rows 2.6 us.
-// ROPE 0: none; 1: RopeView.quads; 2: any.
+// a scale block of 32 channels is two neighbours of one warp (d / 16 is even).  16,384 rows of 576,
+// MXFP4 (19 MB in, 5 MB out): 5.8 us without rotation (8.2 with eight channels a thread: as many
+// instructions for the address and the scale), 9.1 with one axis, 12.2 with three; 32 rows 1.6 to 2.9.
+// At 131,072 rows a scheduler issues in 58%, 69% and 75% of the cycles while DRAM runs at 59%, 41% and
+// 26%: with rotation the issue bounds it, because 4 of a row's 36 threads turn and their warps' others wait.
+// ROPE 0: none; 1: RopeView.quads (the same 16,384 rows through 2: 12.2 us, where 1 takes 9.1); 2: any.
 template <int FMT, int ROPE>
 __global__ void __launch_bounds__(1024) paged_write_kernel(const PagedView C, const uint16_t *x, int64_t ldx,
                                                            int32_t rows, const int32_t *slot,

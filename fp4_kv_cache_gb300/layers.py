@@ -130,7 +130,9 @@ def paged_layer(cache: "paged.PagedCache", state: PagedState, x: PagedInput, win
                 sm_scale: Optional[float] = None, d_status=None, stream=None) -> PagedOutput:
     """A layer over a paged cache, whole contexts or (the schedule's "swa" layers) the last `window`
     rows: the step's bookkeeping, RoPE on the queries, the cache write with RoPE, then attention.
-    Rows of x past the step's last token are neither written nor attended."""
+    Rows of x past the step's last token are neither written nor attended.  Every token is a row of
+    the cache: compressed entries (ratio_m) and rows dropped in front (kv_start) are for callers of
+    paged.paged_attn."""
     T = x.q.shape[0]
     plan = paged.page_plan(state.lens, x.delta, state.block_table, state.free_pages, state.n_free, cache.page, T,
                            in_place=True, d_status=d_status, stream=stream)

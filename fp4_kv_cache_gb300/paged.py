@@ -321,8 +321,9 @@ def paged_attn(q, cache: PagedCache, block_table, lens, cu, pos0=None, d_v: Opti
                want_lse: bool = True, workspace=None, d_status=None, stream=None):
     """Attention of new tokens over their requests' pages -> (out bf16 [n_tokens, heads, d_v],
     lse f32 [n_tokens, heads] or None).  q bf16 [n_tokens, heads, d]; block_table int32 [batch,
-    width]; lens, pos0, kv_start int32 [batch]; cu int32 [batch + 1].  Rows of `out` and `lse`
-    outside every request stay as they were.  See csa2p_attn."""
+    width]; lens, pos0, kv_start int32 [batch]; cu int32 [batch + 1]; d_v: leading channels that are
+    values, at most 512 (None: all d).  Rows of `out` and `lse` outside every request stay as they
+    were.  See csa2p_attn."""
     dev, lib = cache._on_gpu(), _ready or _lib()
     if q.dim() != 3 or q.shape[2] != cache.d or block_table.dim() != 2:
         raise ValueError("q is [n_tokens, heads, the cache's d], block_table [batch, width]")
