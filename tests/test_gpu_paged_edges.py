@@ -78,6 +78,30 @@ def test_plan_steps_with_shortages(B, page, n_pages, most, n_rows, seed, in_plac
     run_plan(steps, [0] * B, [[-1] * width for _ in range(B)], list(range(n_pages)), n_pages, page, n_rows, in_place)
 
 
+@pytest.mark.parametrize("own_lens", [False, True])
+def test_plan_of_several_ctas_captured(own_lens):
+    # replayed with new deltas, pages running out on the way: lengths (or not) and count overwrite the old ones
+    B, page, W, n_rows, n_pages = 6, 4, 500, 5000, 900
+    lens, t_n, t_table, t_free = ints([0] * B), ints([n_pages]), ints([[-1] * W] * B), ints(range(n_pages))
+    buf = torch.empty(B + 1 + 3 * n_rows, dtype=I32, device=DEV)
+    cu, *rows = torch.split(buf, [B + 1, n_rows, n_rows, n_rows])
+    plan, delta, st = paged.PagePlan(ints([0] * B) if own_lens else lens, cu, *rows, t_n), ints([0] * B), status()
+    paged.page_plan(lens, delta, t_table, t_free, t_n, page, n_rows, plan=plan, d_status=st)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        paged.page_plan(lens, delta, t_table, t_free, t_n, page, n_rows, plan=plan, d_status=st)
+    at, table, free = [0] * B, [[-1] * W for _ in range(B)], list(range(n_pages))
+    for d in ([1000, 500, 9, 0, 30, 1], [800, 700, 900, 3, 0, -1], [-100, 40, -700, 0, 900, 5], [-10**6] * 3 + [1, 1, 1], [5] * B):
+        delta.copy_(ints(d)), st.zero_()
+        g.replay()
+        slots, want = plan_step(at, d, table, free, page)
+        assert int(st) == want and plan.lens.tolist() == at and int(t_n) == len(free)
+        assert t_table.tolist() == table and t_free.tolist()[:len(free)] == free
+        assert plan.slot.tolist() == slots + [-1] * (n_rows - len(slots)) and int(plan.cu[0]) == 0
+        lens.copy_(plan.lens)
+
+
 def test_plan_in_place_into_a_plan():
     # in_place overwrites lens and n_free: a plan with others is refused, nothing is done
     table, free, lens, n = ints([[-1] * 4] * 2), ints(range(8)), ints([0, 0]), ints([8])
