@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import csa2, paged
+from . import csa2, draft, paged
 
 
 @dataclass
@@ -155,6 +155,44 @@ def _paged_attend(cache, state, x, plan, window, d_v, sm_scale, d_status, stream
     out, lse = paged.paged_attn(q, cache, state.block_table, state.lens, plan.cu, d_v=d_v, window=window,
                                 sm_scale=sm_scale, d_status=d_status, stream=stream)
     return PagedOutput(out, lse, plan)
+
+
+@dataclass
+class DraftPlan:
+    """A step of drafted tokens, shared by the layers that hold the same rows."""
+    plan: "paged.PagePlan"
+    tree: "draft.TreePlan"
+
+
+def draft_plan(page: int, state: PagedState, x: PagedInput, parent: torch.Tensor, max_nodes: int, d_status=None,
+               stream=None) -> DraftPlan:
+    """A step's new tokens are trees: slots for all nodes (x.delta of each request), their positions and
+    masks.  parent int32 [T]: the node that each follows, counted from its request's first, or -1."""
+    T = x.q.shape[0]
+    plan = paged.page_plan(state.lens, x.delta, state.block_table, state.free_pages, state.n_free, page, T,
+                           in_place=True, d_status=d_status, stream=stream)
+    return DraftPlan(plan, draft.tree_plan(parent, state.lens, plan.cu, max_nodes, d_status, stream))
+
+
+def draft_layer(cache: "paged.PagedCache", state: PagedState, x: PagedInput, step: DraftPlan, window: int = 0, d_v: int = 512,
+                sm_scale: Optional[float] = None, d_status=None, stream=None) -> PagedOutput:
+    """paged_layer for trees: RoPE on the queries at the nodes' positions (x.pos None), the cache write with
+    RoPE, then attention in which a node sees the rows before its tree and the nodes above it."""
+    q, pos = x.q, x.pos
+    if x.cos_sin is not None:
+        pos = step.tree.pos if pos is None else pos
+        q = paged.rope_axes(q, pos, x.cos_sin, x.sections, None, d_status, stream)
+    paged.paged_write(cache, x.x, step.plan.slot, pos, x.cos_sin, x.sections, d_status, stream)
+    out, lse = draft.tree_attn(q, cache, state.block_table, state.lens, step.plan.cu, step.tree.seen, step.tree.pos, d_v=d_v,
+                               window=window, sm_scale=sm_scale, d_status=d_status, stream=stream)
+    return PagedOutput(out, lse, step.plan)
+
+
+def draft_accept(caches, state: PagedState, step: DraftPlan, verdict: "draft.Verdict", d_status=None, stream=None) -> "paged.PagePlan":
+    """The verdict's path becomes the requests' rows in all caches, the other nodes' rows are given back."""
+    draft.paged_compact(caches, state.block_table, state.lens, step.plan.cu, verdict.path, verdict.keep, d_status, stream)
+    return paged.page_plan(state.lens, verdict.delta, state.block_table, state.free_pages, state.n_free, caches[0].page, 0,
+                           in_place=True, d_status=d_status, stream=stream)
 
 
 # The report's schedule (§4.2.1; the review page's zero-based table): layers 0-1 SWA only;
