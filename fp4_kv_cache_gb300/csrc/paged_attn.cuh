@@ -68,7 +68,6 @@ struct TileAt {                          // a key tile, for everyone
     int32_t key0;
     uint32_t flags;                      // kFirst ..
     int32_t nt;                          // key tiles of the row tile, over all CTAs
-    int32_t base, node0;                 // trees: rows before the nodes', the request's first token
 };
 constexpr uint32_t kFirst = 1, kLast = 2;     // of this CTA's key tiles of the row tile
 constexpr uint32_t kEdge = 4;                 // some row does not see every key
@@ -87,14 +86,14 @@ struct AttnParams {
     uint32_t f0, f4;              // see decode
     const uint16_t *q;
     const int32_t *table, *lens, *cu, *pos0, *start;
-    const uint32_t *seen;         // trees: [n_tokens, words] a node's mask, positions where there is a window
-    const int32_t *pos;
-    int32_t words;
     uint16_t *out;
     float *lse;
     uint32_t *d_status;
     float *part_o, *part_ml;      // [2 CTAs][64][d_v], [2 CTAs][64][2]
     PartDesc *desc;               // [CTAs]
+    const uint32_t *seen;         // trees: [n_tokens, words] a node's mask, positions where there is a window
+    const int32_t *pos;
+    int32_t words;
 };
 
 // ------------------------------------------------------------------ PTX
@@ -194,7 +193,15 @@ __device__ __forceinline__ float warp_reduce16(float (&v)[16], int lane)
 }
 
 // ------------------------------------------------------------------ the work list
-struct Item {                 // a row tile
+template <bool TREE>
+struct TreeItem {};
+template <>
+struct TreeItem<true> {
+    int32_t base, first;      // rows before the nodes', the request's first token
+    int32_t nodes, tokens;    // nodes that some row may see, nodes of the request
+};
+template <bool TREE>
+struct Item : TreeItem<TREE> {        // a row tile
     int32_t b, j;             // request, row tile of it
     int32_t rows;             // rows of the tile (1..64)
     int32_t len;              // rows of the cache that the table can reach
@@ -202,7 +209,6 @@ struct Item {                 // a row tile
     int32_t lo, hi;           // keys that some row of the tile may see
     int32_t lo_all, hi_all;   // keys that every row of the tile sees
     int32_t nt;               // key tiles, from lo on (at least one, maybe of no key)
-    int32_t base, first;      // trees: rows before the nodes', the request's first token
     bool more;                // the request has further row tiles
     bool beyond;              // rows past the table may be visible
 };
@@ -243,7 +249,7 @@ __device__ __forceinline__ void bounds(const AttnParams &P, int64_t p, int32_t l
     if (P.window > 0 && e - P.window > lo) lo = e - P.window;
 }
 // Trees: the lowest row before the nodes' that token t of the call sees, where there are so many.
-__device__ __forceinline__ int32_t tree_low(const AttnParams &P, int64_t t, int32_t start)
+__device__ __forceinline__ int32_t tree_low(const AttnParams &P, int32_t t, int32_t start)
 {
     int64_t lo = start > 0 ? start : 0;
     if (P.window > 0) {
@@ -252,10 +258,23 @@ __device__ __forceinline__ int32_t tree_low(const AttnParams &P, int64_t t, int3
     }
     return (int32_t)lo;                                    // positions are below 2^31
 }
-template <bool TREE>
-__device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
+// Word w of the nodes that some row of a row tile sees, from the masks of its tokens t0 .. t1.  Beyond
+// kUnion words in all, every node counts: looking for less would take longer than their keys.
+constexpr int kUnion = 32;
+__device__ __forceinline__ uint32_t tree_union(const AttnParams &P, int32_t t0, int32_t t1, int32_t tokens, int w)
 {
-    Item it;
+    const int32_t left = tokens - 32 * w;
+    const uint32_t all = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
+    if ((t1 - t0 + 1) * P.words > kUnion) return all;
+    uint32_t u = 0;
+#pragma unroll 1
+    for (int32_t t = t0; t <= t1; ++t) u |= P.seen[(int64_t)t * P.words + w];
+    return u & all;
+}
+template <bool TREE>
+__device__ __noinline__ Item<TREE> load_item(const AttnParams &P, int b, int j)
+{
+    Item<TREE> it;
     it.b = b;
     it.j = j;
     int32_t first, tokens;
@@ -273,20 +292,27 @@ __device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
     const int32_t start = P.start ? P.start[b] : 0;
     const uint32_t r0 = (uint32_t)j * kRows;               // rows of a call are fewer than 2^31
     const uint32_t t0 = r0 / (uint32_t)P.H, t1 = (r0 + it.rows - 1) / (uint32_t)P.H;
-    if (TREE) {
-        // Every row before the nodes' and all of theirs: masks decide about the latter.
+    if constexpr (TREE) {
+        // The rows before the nodes' first, then the nodes that some row sees, one behind another: with
+        // 64 heads a tile's rows are one token, so a window of 128 is one tile, and wide trees cost each
+        // of their tokens only its own way up.
         it.base = held - tokens;
         it.first = first;
+        it.tokens = tokens;
+        it.nodes = 0;
         int32_t low = tree_low(P, first + t0, start), high = low;
         for (uint32_t t = t0 + 1; P.window > 0 && t <= t1; ++t) {
             const int32_t l = tree_low(P, first + t, start);
             low = min(low, l);
             high = max(high, l);
         }
-        it.hi = it.len;
-        it.lo = min(min(low, it.base), it.hi);
+        if (it.base < it.len)
+#pragma unroll 1
+            for (int w = 0; 32 * w < tokens; ++w) it.nodes += __popc(tree_union(P, first + t0, first + t1, tokens, w));
+        it.hi = min(it.base, it.len) + it.nodes;
+        it.lo = min(low, min(it.base, it.len));
         it.lo_all = high;
-        it.hi_all = min(it.base, it.hi);
+        it.hi_all = min(it.base, it.len);
         it.beyond = held > it.len;
         it.nt = it.hi > it.lo ? (it.hi - it.lo - 1) / kKeys + 1 : 1;
         return it;
@@ -306,7 +332,7 @@ __device__ __noinline__ Item load_item(const AttnParams &P, int b, int j)
 // Walks a CTA's run of (row tile, key tile) units.
 template <bool TREE>
 struct Walk {
-    Item it;
+    Item<TREE> it;
     int32_t off, n;           // this CTA's key tiles of the item: off .. off + n - 1
     int64_t left;             // units of the run after them
     int32_t at;               // tile of the item
@@ -348,14 +374,20 @@ struct Walk {
 };
 
 template <bool TREE>
-struct Misc {
+struct TreeMisc {};
+template <>
+struct TreeMisc<true> {
+    uint2 see[kRing][kKeys];            // rows that see a key, in tiles that not every row sees whole
+};
+template <bool TREE>
+struct Misc : TreeMisc<TREE> {
     uint64_t full_k[5];                 // chunk pairs and chunk 8 staged
     uint64_t s_done, pv_done[4], full_p, rows[kRing], drained;
     uint2 row[kRing][kKeys];            // where a key's row lies: codes / 16 bytes, scales; kNoRow: no key
     TileAt tile[kRing];
     alignas(16) float m[kRows], nm[kRows], fac[kRows];   // maximum (log2), its negative, factor of a move
     float red[4][kRows];
-    alignas(16) int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile; trees: hi is its token
+    alignas(16) int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile (not of trees)
     int64_t scan[kThreads / 32];
     int64_t item_unit;                  // first unit of this CTA's first item
     Walk<TREE> walk[4];                       // of the upper half's warps: two tiles ahead
@@ -749,10 +781,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const int32_t key0 = walk.key0();
             const uint32_t k = (uint32_t)key0 + key_in;
             uint2 at = make_uint2(kNoRow, 0u);
-            if (k < (uint32_t)walk.it.hi) {
-                const int32_t id = P.table[(int64_t)walk.it.b * P.width + (k >> P.C.shift)];
+            uint32_t row = k;
+            if constexpr (TREE) {
+                if (key0 < walk.it.lo_all || key0 > walk.it.hi_all - kKeys) {
+                    const int32_t row0 = (int32_t)walk.it.row0;                    // rows of a call are fewer than 2^31
+                    const int32_t t0 = (uint32_t)row0 / (uint32_t)P.H, t1 = (uint32_t)(row0 + walk.it.rows - 1) / (uint32_t)P.H;
+                    int32_t node = -1, key_pos = (int32_t)k;
+                    if (k >= (uint32_t)walk.it.base && k < (uint32_t)walk.it.hi) { // the (k - base)-th node of the union
+                        int32_t left = (int32_t)(k - walk.it.base);
+                        int w = 0;
+                        uint32_t u = tree_union(P, t0, t1, walk.it.tokens, 0);
+#pragma unroll 1
+                        while (left >= __popc(u) && 32 * (w + 1) < walk.it.tokens) {
+                            left -= __popc(u);
+                            u = tree_union(P, t0, t1, walk.it.tokens, ++w);
+                        }
+#pragma unroll 1
+                        for (; left > 0; --left) u &= u - 1;
+                        row = kNoRow;                                              // (it.nodes counts them: there is one)
+                        if (u) {
+                            node = 32 * w + __ffs((int)u) - 1;
+                            row = walk.it.base + node;
+                            key_pos = P.window > 0 ? P.pos[walk.it.first + node] : (int32_t)row;
+                        }
+                    }
+                    // the tile's rows, token by token
+                    const int32_t start = P.start ? P.start[walk.it.b] : 0;
+                    uint64_t see = 0;
+                    int32_t r0 = 0;
+#pragma unroll 1
+                    for (int32_t t = t0; t <= t1; ++t) {
+                        const bool bit = node < 0 || (P.seen[(int64_t)t * P.words + (node >> 5)] >> (node & 31) & 1u);
+                        const int32_t r1 = min((t + 1) * P.H - row0, kRows);
+                        if (bit && key_pos >= tree_low(P, t, start)) see |= (~0ull >> (kRows - (r1 - r0))) << r0;
+                        r0 = r1;
+                    }
+                    M.see[ahead_ring][key_in] = make_uint2((uint32_t)see, (uint32_t)(see >> 32));
+                }
+            }
+            if (TREE ? row < (uint32_t)walk.it.len && k < (uint32_t)walk.it.hi : k < (uint32_t)walk.it.hi) {
+                const int32_t id = P.table[(int64_t)walk.it.b * P.width + (row >> P.C.shift)];
                 if (id >= 0 && id < P.C.n_pages) {
-                    const uint32_t in = k & ((1u << P.C.shift) - 1);
+                    const uint32_t in = row & ((1u << P.C.shift) - 1);
                     at.x = (uint32_t)((id * P.C.code_page + (int64_t)in * P.C.code_row) >> 4);
                     at.y = (uint32_t)(id * P.C.scale_page + (int64_t)in * P.C.scale_row);
                 } else {
@@ -762,12 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             M.row[ahead_ring][key_in] = at;
             if (walk.first()) {
                 ++ib;
-                if (TREE && key_in < kRows) {         // rows past the last: as the last
-                    const int64_t t = (walk.it.row0 + min(key_in, walk.it.rows - 1)) / P.H;
-                    M.lo[ib & 3][key_in] = tree_low(P, t, P.start ? P.start[walk.it.b] : 0);
-                    M.hi[ib & 3][key_in] = (int32_t)t;
-                    if (walk.it.beyond) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
-                } else if (key_in < kRows) {          // likewise
+                if constexpr (TREE) {
+                    if (walk.it.beyond && key_in == 0) dev_flag(P.d_status, CSA2_DEV_BAD_INDEX);
+                } else if (key_in < kRows) {          // rows past the last: as the last
                     int32_t hi;
                     int64_t lo, e;
                     const uint32_t f = (uint32_t)walk.it.j * kRows + min(key_in, walk.it.rows - 1);
@@ -788,10 +855,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 t.item = ib & 3;
                 t.key0 = key0;
                 t.nt = walk.it.nt;
-                if (TREE) {
-                    t.base = walk.it.base;
-                    t.node0 = walk.it.first;
-                }
                 t.flags = (walk.first() ? kFirst : 0) | (walk.last() ? kLast : 0) |
                           (key0 < walk.it.lo_all || key0 > walk.it.hi_all - kKeys ? kEdge : 0) | (walk.off > 0 ? kTail : 0) |
                           (walk.off > 0 || walk.off + walk.n < walk.it.nt ? kPart : 0);
@@ -855,10 +918,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             // ---- logits that a row does not see become -inf, those of a key that is not finite NaN
             if (masked) {
                 const int32_t key = (int32_t)((uint32_t)T.key0 + key_in), item = T.item;
-                // trees: the key's node (below 0: none), its position, the word of a mask that has its bit
-                const int32_t node = TREE ? key - T.base : -1;
-                const int32_t key_pos = TREE && have && node >= 0 && P.window > 0 ? P.pos[T.node0 + node] : key;
-                const uint32_t *word = TREE && node >= 0 ? P.seen + (node >> 5) : nullptr;
+                if constexpr (TREE) {
+                    uint32_t is = have ? 0xffffffffu : 0u;
+                    if (have && (flags & kEdge)) is = half ? M.see[ring][key_in].y : M.see[ring][key_in].x;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 32; c0 += 16) {
+                        uint32_t r[16];
+                        tc::tc_ld_32x32b_x16(lane_t + c0, r);
+                        tc::tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) r[c] = !(is >> c & 1u) ? 0xff800000u : nan ? 0x7fc00000u : r[c];
+                        tc::tc_st_32x32b_x16(lane_t + c0, r);
+                        is >>= 16;
+                    }
+                } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < 32; c0 += 16) {
                     uint32_t r[16];
@@ -868,18 +941,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     for (int c = 0; c < 16; c += 4) {
                         const int4 lo = *reinterpret_cast<const int4 *>(&M.lo[item][c_lo + c0 + c]);
                         const int4 hi = *reinterpret_cast<const int4 *>(&M.hi[item][c_lo + c0 + c]);
-                        auto seen = [&](uint32_t x, int l, int h) {
-                            bool is;
-                            if (TREE) is = have && key_pos >= l && (node < 0 || ((word[(int64_t)h * P.words] >> (node & 31)) & 1u));
-                            else is = have && key >= l && key < h;
-                            return !is ? 0xff800000u : nan ? 0x7fc00000u : x;
-                        };
+                        auto seen = [&](uint32_t x, int l, int h) { return !(have && key >= l && key < h) ? 0xff800000u : nan ? 0x7fc00000u : x; };
                         r[c] = seen(r[c], lo.x, hi.x);
                         r[c + 1] = seen(r[c + 1], lo.y, hi.y);
                         r[c + 2] = seen(r[c + 2], lo.z, hi.z);
                         r[c + 3] = seen(r[c + 3], lo.w, hi.w);
                     }
                     tc::tc_st_32x32b_x16(lane_t + c0, r);
+                }
                 }
                 tc::tc_wait_st();
             }
