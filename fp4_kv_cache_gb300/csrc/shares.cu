@@ -44,15 +44,18 @@ __device__ __forceinline__ ForkOf fork_of(const csa2d_share_args &P, int shift, 
     return f;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // One CTA: who is forked, which free page each takes, the new lengths.  A thread has `per` consecutive
 // requests.  What it writes -- lengths and last entries of forked requests -- nobody else reads here: a
 // source is no forked request.
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     __shared__ int32_t s_warp[kForkThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_allow_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n_free = min(max(P.n_free[0], 0), P.free_cap);
     const int per = (P.batch + kForkThreads - 1) / kForkThreads, b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
     uint32_t flags = 0;
@@ -101,47 +104,69 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_sha
     if (tid == 0) P.n_free[0] = max(n_free - all, 0);
 }
 
-// The full pages of forked requests: a CTA a request, or several where its table row is long.
-constexpr int kPagesThreads = 256, kPagesEach = 8;
+// Table rows are gone through in pieces of a warp's kPiece entries, kAhead a lane, all under way at once,
+// by a kernel of its own: one cluster that did this too was slower however few the pieces (a fork and its
+// end, 9 requests of 512 entries: 13.8 us where these four launches take 11.8; 1,000 of 200: 41 and 16).
+constexpr int kAhead = 8, kPiece = 32 * kAhead;
+__device__ __forceinline__ int32_t pieces(int32_t width) { return (width - 1) / kPiece + 1; }
+
+// The full pages of forked request b among the entries of a piece.
+__device__ __forceinline__ void fork_pages(const csa2d_share_args &P, const int shift, int b, int32_t piece, uint32_t *d_status)
+{
+    const int32_t a = P.source[b];
+    if (a < 0 || P.dst[b] == kRefused) return;
+    const int32_t full = P.lens[b] >> shift, n = full - piece * kPiece, lane = threadIdx.x & 31;
+    const int32_t *from = P.block_table + (int64_t)a * P.width + piece * kPiece;
+    int32_t *to = P.block_table + (int64_t)b * P.width + piece * kPiece;
+    int32_t id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) id[k] = lane + 32 * k < n ? from[lane + 32 * k] : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        if (lane + 32 * k < n) to[lane + 32 * k] = id[k];
+        if (id[k] >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        else if (id[k] >= 0) atomicAdd(P.shares + id[k], 1);
+    }
+}
+
+constexpr int kPagesThreads = 256;
 
 __global__ void __launch_bounds__(kPagesThreads) page_share_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
-    const int b = blockIdx.x;
-    const int32_t a = P.source[b];
-    if (a < 0 || P.dst[b] == kRefused) return;
-    const int32_t full = P.lens[b] >> shift;
-    const int32_t *from = P.block_table + (int64_t)a * P.width;
-    int32_t *to = P.block_table + (int64_t)b * P.width;
-    for (int32_t j = blockIdx.y * kPagesThreads + threadIdx.x; j < full; j += gridDim.y * kPagesThreads) {
-        const int32_t id = from[j];
-        to[j] = id;
-        if (id >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        else if (id >= 0) atomicAdd(P.shares + id, 1);
-    }
+    const int32_t n = pieces(P.width);
+    const int64_t i = (int64_t)blockIdx.x * (kPagesThreads / 32) + threadIdx.x / 32;
+    if (i < (int64_t)P.batch * n) fork_pages(P, shift, (int)(i / n), (int)(i % n), d_status);
 }
 
 // ---------------------------------------------------------------- free
-// The pages of ended requests lose a holder each; one without any is marked by a count below 0.
+// The pages of ended request b among the entries of a piece lose a holder each; one without any is
+// marked by a count below 0.
+__device__ __forceinline__ void drop_pages(const csa2d_share_args &P, const int shift, int b, int32_t piece, uint32_t *d_status)
+{
+    if (P.ends[b] == 0) return;
+    const int64_t pages = ((int64_t)max(P.lens[b], 0) + (1 << shift) - 1) >> shift;
+    const int32_t n = (int32_t)min(pages, (int64_t)P.width) - piece * kPiece, lane = threadIdx.x & 31;
+    const int32_t *table = P.block_table + (int64_t)b * P.width + piece * kPiece;
+    int32_t id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) id[k] = lane + 32 * k < n ? table[lane + 32 * k] : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        if (id[k] >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        else if (id[k] >= 0) atomicSub(P.shares + id[k], 1);
+    }
+}
+
 __global__ void __launch_bounds__(kPagesThreads) page_drop_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
-    const int b = blockIdx.x;
-    if (P.ends[b] == 0) return;
-    const int64_t pages = ((int64_t)max(P.lens[b], 0) + (1 << shift) - 1) >> shift;
-    const int32_t held = (int32_t)min(pages, (int64_t)P.width);
-    const int32_t *table = P.block_table + (int64_t)b * P.width;
-    for (int32_t j = blockIdx.y * kPagesThreads + threadIdx.x; j < held; j += gridDim.y * kPagesThreads) {
-        const int32_t id = table[j];
-        if (id >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        else if (id >= 0) atomicSub(P.shares + id, 1);
-    }
+    const int32_t n = pieces(P.width);
+    const int64_t i = (int64_t)blockIdx.x * (kPagesThreads / 32) + threadIdx.x / 32;
+    if (i < (int64_t)P.batch * n) drop_pages(P, shift, (int)(i / n), (int)(i % n), d_status);
 }
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // One cluster: marked pages go on the free list in the order of their ids, so that it does not depend
 // on the order in which the counts fell.  Each CTA has a run of ids; it counts, learns what the runs
@@ -220,7 +245,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const csa2d_sha
 }
 
 // ---------------------------------------------------------------- contents
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 256, kCopyEach = 6;    // loads of 16 bytes a thread has under way
 
 __device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from, int64_t n, int64_t first, int64_t step)
 {
@@ -228,13 +253,13 @@ __device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from, int
     int64_t done = 0;
     if ((low & 15) == 0) {
         done = n & ~(int64_t)15;
-        for (int64_t i = first; i < n / 16; i += 4 * step) {
-            uint4 v[4];
+        for (int64_t i = first; i < n / 16; i += kCopyEach * step) {
+            uint4 v[kCopyEach];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kCopyEach; ++k)
                 if (i + k * step < n / 16) v[k] = reinterpret_cast<const uint4 *>(from)[i + k * step];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kCopyEach; ++k)
                 if (i + k * step < n / 16) reinterpret_cast<uint4 *>(to)[i + k * step] = v[k];
         }
     } else if ((low & 3) == 0) {
@@ -265,11 +290,11 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
     if (C.scale_row) copy_bytes(scales + to * C.scale_page, scales + from * C.scale_page, n * C.scale_row, first, step);
 }
 
-// CTAs a table row: kPagesEach entries a thread.
-unsigned row_ctas(int32_t width)
+// CTAs of a warp for each piece of all the table rows.
+unsigned piece_ctas(const csa2d_share_args &a)
 {
-    const int64_t n = ((int64_t)width + kPagesThreads * kPagesEach - 1) / (kPagesThreads * kPagesEach);
-    return (unsigned)(n < 32 ? n : 32);
+    const int64_t n = (int64_t)a.batch * ((a.width - 1) / kPiece + 1);
+    return (unsigned)((n + kPagesThreads / 32 - 1) / (kPagesThreads / 32));
 }
 
 } // namespace
@@ -279,13 +304,13 @@ cudaError_t launch_page_fork(const csa2d_share_args &a, uint32_t *d_status, cuda
     const int shift = __builtin_ctz((unsigned)a.page);
     const cudaError_t e = launch_pdl(page_fork_kernel, dim3(1), dim3(kForkThreads), 0, s, 1, a, shift, d_status);
     if (e != cudaSuccess) return e;
-    return launch_pdl(page_share_kernel, dim3((unsigned)a.batch, row_ctas(a.width)), dim3(kPagesThreads), 0, s, 1, a, shift, d_status);
+    return launch_pdl(page_share_kernel, dim3(piece_ctas(a)), dim3(kPagesThreads), 0, s, 1, a, shift, d_status);
 }
 
 cudaError_t launch_page_free(const csa2d_share_args &a, uint32_t *d_status, cudaStream_t s)
 {
     const int shift = __builtin_ctz((unsigned)a.page);
-    const cudaError_t e = launch_pdl(page_drop_kernel, dim3((unsigned)a.batch, row_ctas(a.width)), dim3(kPagesThreads), 0, s, 1, a, shift, d_status);
+    const cudaError_t e = launch_pdl(page_drop_kernel, dim3(piece_ctas(a)), dim3(kPagesThreads), 0, s, 1, a, shift, d_status);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_list_kernel, dim3(kListCtas), dim3(kListThreads), 0, s, kListCtas, a, d_status);
 }
@@ -298,7 +323,7 @@ cudaError_t launch_page_copy(const CacheSet &set, int n, const int32_t *src, con
         const int64_t bytes = (int64_t)set.c[i].code_row << set.c[i].shift;
         most = bytes > most ? bytes : most;
     }
-    const int64_t z = (most + kCopyThreads * 64 - 1) / (kCopyThreads * 64);
+    const int64_t z = (most + kCopyThreads * kCopyEach * 16 - 1) / (kCopyThreads * kCopyEach * 16);
     return launch_pdl(page_copy_kernel, dim3((unsigned)count, (unsigned)n, (unsigned)(z < 64 ? z : 64)), dim3(kCopyThreads), 0, s, 1, set, src, dst, rows, d_status);
 }
 

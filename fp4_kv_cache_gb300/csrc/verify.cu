@@ -11,7 +11,9 @@
 // decides about a token.  A weight w is taken apart without 64-bit conversions (which run at a fraction
 // of the rate here): h = w 2^20 rounded to a whole number, and the rest times 2^20, rounded; adding
 // 1.5 2^23 leaves either number in the low bits of a float.  h 2^20 + rest is w 2^40 rounded, ties to
-// even, since h 2^20 is even.
+// even, since h 2^20 is even.  Two weights go through this at a time (add, multiply and fma of two
+// floats are one instruction here); what has to be looked at one by one -- values below 0, above 1 or
+// not finite -- is found by the largest bit pattern of a load.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -43,6 +45,33 @@ __device__ __forceinline__ float clean(float v, bool &bad)
 // What is left of p: max(p - c q, 0), at most 1.
 __device__ __forceinline__ float rest_of(float p, float q, float c) { return fminf(fmaxf(__fsub_rn(p, __fmul_rn(c, q)), 0.0f), 1.0f); }
 
+// Two floats, each operation rounded once for either.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void apart(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
 struct Sum {
     uint32_t high, low;                     // with the offsets of kMagic still in them
 };
@@ -52,6 +81,18 @@ __device__ __forceinline__ void add(Sum &s, float w)
     const float l = __fmaf_rn(__fsub_rn(t, __fsub_rn(h, kMagic)), 1048576.0f, kMagic);
     s.high += __float_as_uint(h);
     s.low += __float_as_uint(l);
+}
+// The same for two weights.
+__device__ __forceinline__ void add(Sum &s, float w0, float w1)
+{
+    const uint64_t k20 = pair(1048576.0f, 1048576.0f), magic = pair(kMagic, kMagic), back = pair(-kMagic, -kMagic), minus = pair(-1.0f, -1.0f);
+    const uint64_t t = mul2(pair(w0, w1), k20), h = add2(t, magic);
+    const uint64_t l = fma2(fma2(add2(h, back), minus, t), k20, magic);       // t - (h - magic), exact
+    float a, b, c, d;
+    apart(h, a, b);
+    apart(l, c, d);
+    s.high += __float_as_uint(a) + __float_as_uint(b);
+    s.low += __float_as_uint(c) + __float_as_uint(d);
 }
 __device__ __forceinline__ int64_t whole(const Sum &s, uint32_t n)
 {
@@ -202,22 +243,53 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const csa2d_verif
     auto sum_row = [&](float cc, bool take) -> int64_t {
         Sum s{0, 0};
         uint32_t count = 0;
-        constexpr int kAhead = VEC == 1 ? 8 : 2;          // loads of a lane under way
+        constexpr int kAhead = VEC == 1 ? 8 : VEC == 4 ? 4 : 2;      // loads of a lane under way
+        const bool two = DRAWN && cc > 0.0f;
+        const uint64_t c2 = pair(-cc, -cc);
+#pragma unroll 1
         for (int32_t x = x0 + VEC * lane; x < x1; x += 32 * VEC * kAhead) {
-            float w[kAhead][VEC];
+            float p[kAhead][VEC], q[kAhead][VEC];
+            uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                if (x + 32 * VEC * k < x1) {
-                    load(x + 32 * VEC * k, cc, w[k]);
-                } else {
+                const int32_t at_x = x + 32 * VEC * k;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) w[k][i] = 0.0f;
+                for (int i = 0; i < VEC; ++i) p[k][i] = q[k][i] = 0.0f;
+                if (at_x + VEC <= x1) {
+                    load_values<T, VEC>(row_p + at_x, p[k]);
+                    if (two) load_values<T, VEC>(row_q + at_x, q[k]);
+                } else if (VEC > 1) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        if (at_x + i < x1) p[k][i] = value(row_p[at_x + i]);
+                        if (at_x + i < x1 && two) q[k][i] = value(row_q[at_x + i]);
+                    }
                 }
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) add(s, w[k][i]);
+                for (int i = 0; i < VEC; ++i) top = max(top, max(__float_as_uint(p[k][i]), __float_as_uint(q[k][i])));
+            if (top > 0x3f800000u) {                      // one by one
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        p[k][i] = clean(p[k][i], bad);
+                        p[k][i] = two ? rest_of(p[k][i], clean(q[k][i], bad), cc) : fminf(p[k][i], 1.0f);
+                        q[k][i] = 0.0f;
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead * VEC; k += 2) {
+                float w0 = p[k / VEC][k % VEC], w1 = p[(k + 1) / VEC][(k + 1) % VEC];
+                if (two) {                                // p + (-(c q)), each rounded: p - c q
+                    apart(add2(pair(w0, w1), mul2(c2, pair(q[k / VEC][k % VEC], q[(k + 1) / VEC][(k + 1) % VEC]))), w0, w1);
+                    w0 = fmaxf(w0, 0.0f);
+                    w1 = fmaxf(w1, 0.0f);
+                }
+                add(s, w0, w1);
+            }
             count += kAhead * VEC;
         }
         int64_t mine = whole(s, count);
@@ -378,9 +450,11 @@ cudaError_t launch(const csa2d_verify_args &a, int ctas, uint32_t *d_status, cud
 
 cudaError_t launch_tree_verify(const csa2d_verify_args &a, uint32_t *d_status, cudaStream_t s)
 {
-    // CTAs a request: as many as fill the GPU a few times, a power of two; none without a few thousand tokens
+    // CTAs a request: a power of two of them, while all requests' fit the GPU at once (two an SM; 64 trees
+    // of 16 nodes over 131,072 tokens: 26.6 us with four, 28.8 with eight, 41 with two; one chain of six:
+    // 10.2 us with eight, 14.4 with four) and each has a few thousand tokens.
     int ctas = kMaxCtas;
-    while (ctas > 1 && ((int64_t)a.batch * ctas > 4 * (int64_t)device_sm_count() || a.vocab < 2048 * ctas)) ctas /= 2;
+    while (ctas > 1 && ((int64_t)a.batch * ctas > 2 * (int64_t)device_sm_count() || a.vocab < 2048 * ctas)) ctas /= 2;
     switch (a.type) {
     case CSA2D_F32: return a.q ? launch<float, true>(a, ctas, d_status, s) : launch<float, false>(a, ctas, d_status, s);
     case CSA2D_F16: return a.q ? launch<__half, true>(a, ctas, d_status, s) : launch<__half, false>(a, ctas, d_status, s);

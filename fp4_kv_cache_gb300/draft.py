@@ -89,12 +89,6 @@ def _lib():
     return _ready
 
 
-def _vector(t, name: str) -> int:
-    if t.dim() != 1:
-        raise ValueError(f"{name} has one dimension, not {tuple(t.shape)}")
-    return t.shape[0]
-
-
 # ------------------------------------------------------------------------------------------ trees
 @dataclass
 class TreePlan:
@@ -107,15 +101,17 @@ def tree_plan(parent, lens, cu, max_nodes: int, d_status=None, stream=None, out:
     """Positions and masks of trees: parent int32 [n_tokens] (a lower node of the request, or -1), lens
     int32 [batch] rows held with the nodes', cu int32 [batch + 1].  max_nodes: of one request, at most
     1,024 (it gives the masks' width).  See csa2d_tree_plan."""
-    dev, T, B = parent.get_device(), _vector(parent, "parent"), _vector(lens, "lens")
+    dev, T, B = parent.get_device(), parent.numel(), lens.numel()
     words = -(-max_nodes // 32)
     if not 1 <= words <= MAX_WORDS:
         raise ValueError(f"max_nodes is 1..{32 * MAX_WORDS}, not {max_nodes}")
     if out is None:
-        buf = _empty(T * (1 + words), _i32, parent.device, stream)
-        out = TreePlan(buf[:T], buf[T:].view(T, words))
+        out = TreePlan(_empty(T, _i32, parent.device, stream), _empty((T, words), _i32, parent.device, stream))
+        at_pos, at_seen = out.pos.data_ptr(), out.seen.data_ptr()
+    else:
+        at_pos, at_seen = _need(out.pos, "out.pos", _i32, T, dev), _need(out.seen, "out.seen", _i32, T * words, dev)
     a = _TREE.pack(B, T, words, _need(parent, "parent", _i32, T, dev), _need(lens, "lens", _i32, B, dev), _need(cu, "cu", _i32, B + 1, dev),
-                   _need(out.pos, "out.pos", _i32, T, dev), _need(out.seen, "out.seen", _i32, T * words, dev))
+                   at_pos, at_seen)
     st = (_ready or _lib()).csa2d_tree_plan(a, _status(d_status, dev), _stream_of(dev, stream))
     if st:
         raise Csa2Error("csa2d_tree_plan", st)
@@ -135,7 +131,7 @@ def tree_attn(q, cache: PagedCache, block_table, lens, cu, seen, pos=None, d_v: 
         raise ValueError("a window needs the nodes' positions")
     T, H, d = q.shape
     d_v = d if d_v is None else d_v
-    B, W, words = _vector(lens, "lens"), block_table.shape[1], seen.shape[1]
+    B, W, words = lens.numel(), block_table.shape[1], seen.shape[1]
     a = _ATTN.pack(*cache.fields, B, T, H, d_v, W, window, words, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale,
                    _need(q, "q", _bf16, None, dev), _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
                    _need(cu, "cu", _i32, B + 1, dev), _need(seen, "seen", _i32, T * words, dev), _maybe(pos, "pos", _i32, T, dev),
@@ -186,7 +182,7 @@ def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = No
     children were drawn from (None: the drafts are certain); token, parent int32 and u f32 [n_tokens];
     cu int32 [batch + 1]; r f32 [batch]; u and r uniform from 0 to 1.  max_path: entries of a path (None:
     n_tokens).  See csa2d_tree_verify."""
-    dev, T, B = p.get_device(), _vector(token, "token"), _vector(r, "r")
+    dev, T, B = p.get_device(), token.numel(), r.numel()
     if p.dtype not in _TYPES or p.dim() != 2:
         raise ValueError("p is float32, float16 or bfloat16 [n_tokens, vocab]")
     V = p.shape[1]
@@ -194,13 +190,16 @@ def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = No
     at_p, p_row = _rows(p, "p", T, V, p.dtype, dev)
     at_q, q_row = (0, V) if q is None else _rows(q, "q", T, V, p.dtype, dev)
     if out is None:
-        buf = _empty(B * (3 + max(max_path, 0)), _i32, p.device, stream)
-        out = Verdict(buf[:B], buf[3 * B:].view(B, max(max_path, 0)), buf[B:2 * B], buf[2 * B:3 * B])
+        keep, token_out, delta = _empty((3, B), _i32, p.device, stream).unbind(0)
+        out = Verdict(keep, _empty((B, max(max_path, 0)), _i32, p.device, stream), token_out, delta)
+        at = keep.data_ptr()
+        at = (at, out.path.data_ptr(), at + 4 * B, at + 8 * B)
+    else:
+        at = (_need(out.keep, "out.keep", _i32, B, dev), _need(out.path, "out.path", _i32, B * max(max_path, 0), dev),
+              _need(out.token, "out.token", _i32, B, dev), _need(out.delta, "out.delta", _i32, B, dev))
     a = _VERIFY.pack(B, T, V, _TYPES[p.dtype], max_path, p_row, q_row, at_p, at_q, _need(token, "token", _i32, T, dev),
                      _need(parent, "parent", _i32, T, dev), _need(cu, "cu", _i32, B + 1, dev), _need(u, "u", _f32, T, dev),
-                     _need(r, "r", _f32, B, dev), _need(out.keep, "out.keep", _i32, B, dev),
-                     _need(out.path, "out.path", _i32, B * max(max_path, 0), dev), _need(out.token, "out.token", _i32, B, dev),
-                     _need(out.delta, "out.delta", _i32, B, dev))
+                     _need(r, "r", _f32, B, dev), *at)
     st = (_ready or _lib()).csa2d_tree_verify(a, _status(d_status, dev), _stream_of(dev, stream))
     if st:
         raise Csa2Error("csa2d_tree_verify", st)
@@ -213,8 +212,11 @@ def _sets(caches: Sequence[PagedCache]):
     if not caches:
         raise ValueError("no cache is given")
     dev = caches[0]._on_gpu()
-    if any(c.index != dev for c in caches):
-        raise ValueError("the caches are on several devices")
+    for c in caches:
+        if c.index != dev:
+            raise ValueError("the caches are on several devices")
+    if len(caches) <= MAX_CACHES:
+        return dev, ((b"".join([c.packed for c in caches]), len(caches)),)
     parts = [caches[i:i + MAX_CACHES] for i in range(0, len(caches), MAX_CACHES)]
     return dev, [(b"".join(c.packed for c in part), len(part)) for part in parts]
 
@@ -224,11 +226,13 @@ def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, kee
     = lens[b] - nodes).  block_table int32 [batch, width], lens and keep int32 [batch], cu int32 [batch +
     1], path int32 [batch, max_path].  See csa2d_compact."""
     dev, sets = _sets(caches)
-    B = _vector(lens, "lens")
+    B = lens.numel()
     if block_table.dim() != 2 or path.dim() != 2:
         raise ValueError("block_table is [batch, width], path [batch, max_path]")
-    if any(c.page != caches[0].page for c in caches):
-        raise ValueError("the caches have pages of several sizes")
+    page = caches[0].page
+    for c in caches:
+        if c.page != page:
+            raise ValueError("the caches have pages of several sizes")
     W, L = block_table.shape[1], path.shape[1]
     a = _COMPACT.pack(B, W, L, _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
                       _need(cu, "cu", _i32, B + 1, dev), _need(path, "path", _i32, B * L, dev), _need(keep, "keep", _i32, B, dev))
@@ -248,12 +252,12 @@ class Fork:
 
 
 def _share(which, name: str, lens, block_table, shares, free_pages, n_free, page: int, fork, out):
-    dev, B = lens.get_device(), _vector(lens, "lens")
+    dev, B = lens.get_device(), lens.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table is [batch, width]")
     W = block_table.shape[1]
     at = _need(which, name, _i32, B, dev)
-    return dev, _SHARE.pack(B, page, W, _vector(shares, "shares"), _vector(free_pages, "free_pages"), at if fork else 0, 0 if fork else at,
+    return dev, _SHARE.pack(B, page, W, shares.numel(), free_pages.numel(), at if fork else 0, 0 if fork else at,
                             _need(lens, "lens", _i32, B, dev), _need(block_table, "block_table", _i32, B * W, dev),
                             _need(shares, "shares", _i32, None, dev), _need(free_pages, "free_pages", _i32, None, dev),
                             _need(n_free, "n_free", _i32, 1, dev), *out)
@@ -264,10 +268,13 @@ def page_fork(source, lens, block_table, shares, free_pages, n_free, page: int, 
     """Requests with source[b] >= 0 take over that request's rows: lens, block_table, shares (int32
     [n_pages], a page's holders beyond the first) and n_free are updated, and the pages to copy are
     returned.  See csa2d_page_fork."""
-    B, dev = _vector(lens, "lens"), lens.get_device()
+    B, dev = lens.numel(), lens.get_device()
     if out is None:
         out = Fork(*_empty((3, B), _i32, lens.device, stream).unbind(0))
-    at = [_need(t, name, _i32, B, dev) for t, name in ((out.src, "out.src"), (out.dst, "out.dst"), (out.rows, "out.rows"))]
+        at = out.src.data_ptr()
+        at = (at, at + 4 * B, at + 8 * B)
+    else:
+        at = (_need(out.src, "out.src", _i32, B, dev), _need(out.dst, "out.dst", _i32, B, dev), _need(out.rows, "out.rows", _i32, B, dev))
     dev, a = _share(source, "source", lens, block_table, shares, free_pages, n_free, page, True, at)
     st = (_ready or _lib()).csa2d_page_fork(a, _status(d_status, dev), _stream_of(dev, stream))
     if st:
@@ -288,7 +295,7 @@ def page_copy(caches: Sequence[PagedCache], src, dst, rows=None, d_status=None, 
     """In every cache the first rows[i] rows (None: all) of page src[i] copied to page dst[i]; pairs with
     a page below 0 are skipped.  int32 [n] each.  See csa2d_page_copy."""
     dev, sets = _sets(caches)
-    n = _vector(src, "src")
+    n = src.numel()
     at = _need(src, "src", _i32, n, dev), _need(dst, "dst", _i32, n, dev), _maybe(rows, "rows", _i32, n, dev) or None
     status, raw = _status(d_status, dev), _stream_of(dev, stream)
     for packed, k in sets:

@@ -27,7 +27,7 @@ DEV_NO_PAGES, DEV_TABLE_FULL, DEV_ROWS = 0x100, 0x200, 0x400
 MAX_BATCH = 16384
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-_i32, _bf16, _f32 = torch.int32, torch.bfloat16, torch.float32
+_i32, _bf16, _f32, _u8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
 # (a torch without CUDA has neither; nothing there gets as far as a stream)
 _raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
@@ -63,6 +63,8 @@ _PLAN = struct.Struct("@5i4x11P")                      # csa2p_plan_args
 _ROPE = struct.Struct("@5i4xPPq")                      # csa2p_rope_axes
 _ATTN = struct.Struct("@" + _CACHE + "7if6P")          # csa2p_attn_args
 _CACHE = struct.Struct("@" + _CACHE)
+
+_FORMATS = {16: MXFP4, 8: NVFP4_E4M3_16, 32: MXFP8}      # by codes a scale
 
 _ready = None
 
@@ -136,30 +138,31 @@ class PagedCache:
     (a view of a larger buffer)."""
 
     def __init__(self, codes: torch.Tensor, scales: Optional[torch.Tensor] = None):
-        if codes.dim() != 3 or (scales is not None and (scales.dim() != 3 or scales.shape[:2] != codes.shape[:2])):
+        shape = codes.shape
+        if len(shape) != 3:
             raise ValueError("codes and scales are [n_pages, page, bytes of a row]")
-        n, page, w = codes.shape
+        n, page, w = shape
+        index = codes.get_device()                    # -1: not on a GPU
         if scales is None:
-            if codes.dtype != torch.bfloat16:
+            if codes.dtype is not _bf16:
                 raise ValueError("a cache without scales holds bf16 values")
-            fmt, d = BF16, w
+            fmt, d, at_scales, scale_pages = BF16, w, 0, 0
         else:
-            if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or scales.device != codes.device:
+            more = scales.shape
+            if len(more) != 3 or more[0] != n or more[1] != page:
+                raise ValueError("codes and scales are [n_pages, page, bytes of a row]")
+            if codes.dtype is not _u8 or scales.dtype is not _u8 or scales.get_device() != index or (index < 0 and scales.device != codes.device):
                 raise ValueError("codes and scales are uint8 tensors on one device")
-            ratio = w / scales.shape[2] if scales.shape[2] else 0
-            try:
-                fmt = {16: MXFP4, 8: NVFP4_E4M3_16, 32: MXFP8}[ratio]
-            except KeyError:
-                raise ValueError("the widths of codes and scales fit no row format") from None
+            fmt = _FORMATS.get(w / more[2] if more[2] else 0)
+            if fmt is None:
+                raise ValueError("the widths of codes and scales fit no row format")
             d = w if fmt == MXFP8 else 2 * w
-        code_pages, scale_pages = self._pages(codes, n, page, w), 0
-        if scales is not None:
-            scale_pages = self._pages(scales, n, page, scales.shape[2])
+            at_scales, scale_pages = scales.data_ptr(), self._pages(scales, n, page, more[2])
+        code_pages = self._pages(codes, n, page, w)
         self.codes, self.scales, self.fmt, self.d, self.page, self.n_pages = codes, scales, fmt, d, page, n
         self.device = codes.device
-        self.index = codes.get_device()               # -1: not on a GPU
-        self.fields = (fmt, d, page, n, codes.data_ptr(), scales.data_ptr() if scales is not None else 0,
-                       2 * code_pages if fmt == BF16 else code_pages, scale_pages)
+        self.index = index
+        self.fields = (fmt, d, page, n, codes.data_ptr(), at_scales, 2 * code_pages if fmt == BF16 else code_pages, scale_pages)
         self.packed = _CACHE.pack(*self.fields)
 
     @staticmethod
