@@ -11,7 +11,8 @@ namespace {
 constexpr int32_t kRefused = -2;            // in dst: the request was not forked
 
 // ---------------------------------------------------------------- fork
-constexpr int kForkThreads = 512;
+constexpr int kForkThreads = 1024;
+static_assert(kForkThreads == 32 * 32, "a lane for each warp");
 
 struct ForkOf {
     int32_t from, len;                      // -1: no fork
@@ -47,41 +48,36 @@ __device__ __forceinline__ ForkOf fork_of(const csa2d_share_args &P, int shift, 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// One CTA: who is forked, which free page each takes, the new lengths.  A thread has `per` consecutive
-// requests.  What it writes -- lengths and last entries of forked requests -- nobody else reads here: a
-// source is no forked request.
+// One CTA: who is forked, which free page each takes, the new lengths; a thread has one of 1,024
+// requests at a time.  What it writes -- lengths and last entries of forked requests -- nobody else
+// reads here: a source is no forked request.  Latency bounds it: source, lengths, last page, scan, page.
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     __shared__ int32_t s_warp[kForkThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_allow_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n_free = min(max(P.n_free[0], 0), P.free_cap);
-    const int per = (P.batch + kForkThreads - 1) / kForkThreads, b0 = min(tid * per, P.batch), b1 = min(b0 + per, P.batch);
     uint32_t flags = 0;
-    int32_t own = 0;
-    for (int b = b0; b < b1; ++b) own += fork_of(P, shift, b).page;
-    int32_t before = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t u = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += u;
-    }
-    if (lane == 31) s_warp[warp] = before;
-    before -= own;
-    __syncthreads();
-    int32_t all = 0;
-    for (int w = 0; w < kForkThreads / 32; ++w) {
-        if (w < warp) before += s_warp[w];
-        all += s_warp[w];
-    }
-    for (int b = b0; b < b1; ++b) {
-        const ForkOf f = fork_of(P, shift, b);
-        int32_t src = -1, dst = -1, rows = 0;
+    int32_t all = 0;                                       // pages taken by the requests before
+    for (int b0 = 0; b0 < P.batch; b0 += kForkThreads) {
+        const int b = b0 + tid;
+        const bool is = b < P.batch;
+        ForkOf f{-1, 0, 0u, false, -1};
+        if (is) f = fork_of(P, shift, b);
         flags |= f.flags;
+        const uint32_t take = __ballot_sync(0xffffffffu, f.page);
+        if (lane == 0) s_warp[warp] = __popc(take);
+        __syncthreads();
+        // every warp sums up all warps' numbers
+        const int32_t mine = s_warp[lane];
+        const int32_t earlier = (int32_t)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)mine : 0u);
+        const int32_t at = n_free - 1 - (all + earlier + __popc(take & ((1u << lane) - 1)));
+        all += (int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)mine);
+        __syncthreads();                                   // read before the next requests' are written
+        if (!is) continue;
+        int32_t src = -1, dst = -1, rows = 0;
         if (P.source[b] >= 0) {
-            const int32_t at = n_free - 1 - before;
-            before += f.page;
             if (f.from < 0 || (f.page && at < 0)) {
                 dst = kRefused;
                 if (f.from >= 0) flags |= CSA2P_DEV_NO_PAGES;
@@ -101,6 +97,7 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_sha
         P.rows[b] = rows;
     }
     if (flags) dev_flag(d_status, flags);
+    __syncthreads();                                       // n_free has been read (a call without requests has no other)
     if (tid == 0) P.n_free[0] = max(n_free - all, 0);
 }
 

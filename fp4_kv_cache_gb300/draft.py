@@ -3,7 +3,8 @@
 As in ``paged``: the helpers check what they are given, allocate outputs with torch and call the C
 entry points; work goes to the current CUDA stream (or the one given) of the current device, which
 has to be the tensors'.  ``layers.draft_plan``, ``draft_layer`` and ``draft_accept`` string them
-together with the paged cache's calls.
+together with the paged cache's calls.  Outputs are tensors of their own: three allocations take less
+of the host's time than one and its views.
 """
 from __future__ import annotations
 
@@ -190,10 +191,10 @@ def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = No
     at_p, p_row = _rows(p, "p", T, V, p.dtype, dev)
     at_q, q_row = (0, V) if q is None else _rows(q, "q", T, V, p.dtype, dev)
     if out is None:
-        keep, token_out, delta = _empty((3, B), _i32, p.device, stream).unbind(0)
-        out = Verdict(keep, _empty((B, max(max_path, 0)), _i32, p.device, stream), token_out, delta)
-        at = keep.data_ptr()
-        at = (at, out.path.data_ptr(), at + 4 * B, at + 8 * B)
+        device = p.device
+        out = Verdict(_empty(B, _i32, device, stream), _empty((B, max(max_path, 0)), _i32, device, stream), _empty(B, _i32, device, stream),
+                      _empty(B, _i32, device, stream))
+        at = (out.keep.data_ptr(), out.path.data_ptr(), out.token.data_ptr(), out.delta.data_ptr())
     else:
         at = (_need(out.keep, "out.keep", _i32, B, dev), _need(out.path, "out.path", _i32, B * max(max_path, 0), dev),
               _need(out.token, "out.token", _i32, B, dev), _need(out.delta, "out.delta", _i32, B, dev))
@@ -270,9 +271,9 @@ def page_fork(source, lens, block_table, shares, free_pages, n_free, page: int, 
     returned.  See csa2d_page_fork."""
     B, dev = lens.numel(), lens.get_device()
     if out is None:
-        out = Fork(*_empty((3, B), _i32, lens.device, stream).unbind(0))
-        at = out.src.data_ptr()
-        at = (at, at + 4 * B, at + 8 * B)
+        device = lens.device
+        out = Fork(_empty(B, _i32, device, stream), _empty(B, _i32, device, stream), _empty(B, _i32, device, stream))
+        at = (out.src.data_ptr(), out.dst.data_ptr(), out.rows.data_ptr())
     else:
         at = (_need(out.src, "out.src", _i32, B, dev), _need(out.dst, "out.dst", _i32, B, dev), _need(out.rows, "out.rows", _i32, B, dev))
     dev, a = _share(source, "source", lens, block_table, shares, free_pages, n_free, page, True, at)
