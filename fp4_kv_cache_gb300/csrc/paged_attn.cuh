@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     const int32_t start = P.start ? P.start[walk.it.b] : 0;
                     uint64_t see = 0;
                     int32_t r0 = 0;
-#pragma unroll 1
+#pragma unroll 4
                     for (int32_t t = t0; t <= t1; ++t) {
                         const bool bit = node < 0 || (P.seen[(int64_t)t * P.words + (node >> 5)] >> (node & 31) & 1u);
                         const int32_t r1 = min((t + 1) * P.H - row0, kRows);

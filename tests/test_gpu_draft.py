@@ -234,6 +234,33 @@ def test_tree_attn_masks_of_the_callers(kind, H, window):
         assert bool((out[45:90] == 0).all()) and bool((lse[45:90] == -math.inf).all())
 
 
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("H,lens,sizes,max_nodes", [(64, [400], [300], 1024), (128, [350, 90], [300, 40], 320), (16, [260], [200], 192 + 8), (16, [260], [200], 256),
+                                                    (1, [700], [640], 1024), (8, [130, 257], [130, 128], 130)])
+@pytest.mark.parametrize("kind", ["tree", "holes"])
+def test_tree_attn_wide_masks(kind, H, lens, sizes, max_nodes, window):
+    # masks of many words, where a row tile's tokens are looked through for the nodes they see, and where not
+    def mask(r, seen):
+        return np.where(r.random(seen.shape) < 0.7, 0, r.integers(0, 2**32, seen.shape, dtype=np.uint32) & r.integers(0, 2**32, seen.shape, dtype=np.uint32)).astype(np.uint32)
+    check(TreeCase(lens, sizes, H, 128, 128, paged.MXFP8, 32, window, None, seed=H + max_nodes, max_nodes=max_nodes, mask=mask if kind == "holes" else None))
+
+
+@pytest.mark.parametrize("fmt", [paged.MXFP4, paged.BF16])
+def test_tree_attn_strided_pages(fmt):
+    c = TreeCase([300, 100], [25, 6], 64, 576, 512, fmt, 16, seed=14)
+    want, n = c.run(), c.cache.n_pages
+    codes = torch.zeros((n, 3, 16, c.cache.codes.shape[2]), device=DEV, dtype=c.cache.codes.dtype)
+    codes[:, 2] = c.cache.codes
+    if fmt == paged.BF16:
+        c.cache = paged.PagedCache(codes[:, 2])
+    else:
+        scales = torch.full((n, 2, 16, c.cache.scales.shape[2]), 255, device=DEV, dtype=torch.uint8)
+        scales[:, 1] = c.cache.scales
+        c.cache = paged.PagedCache(codes[:, 2], scales[:, 1])
+    got = c.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_tree_attn_of_a_chain_is_paged_attn():
     c = TreeCase([3000, 400], [6, 6], 64, 576, 512, paged.MXFP4, 64, shape="chain", seed=3)
     out, lse = c.run()
@@ -956,6 +983,21 @@ def test_pages_captured():
         P.lens = [0 if x else n for x, n in zip(e, lens)]
         assert P.t_lens.tolist() == P.lens
     assert sorted(P.t_free.tolist()) == list(range(100)) and int(P.t_n) == 100 and P.t_shares.tolist() == [0] * 100
+
+
+def test_many_requests():
+    # as many as a call takes: offsets, scans and tiles of 1,024 requests
+    B, page, W = paged.MAX_BATCH, 4, 3
+    r, n_pages = np.random.default_rng(8), 40000
+    P = Pages(B, W, n_pages, page)
+    P.grow([int(v) if b % 5 == 0 else 0 for b, v in enumerate(r.integers(1, W * page, B))])
+    P.fork([-1 if b % 5 == 0 else int(r.integers(0, B // 5)) * 5 if r.random() < 0.9 else int(r.integers(0, B)) for b in range(B)])
+    P.end([int(v) for v in r.random(B) < 0.5])
+    P.end([1] * B)
+    sizes = [int(v) for v in r.integers(0, 3, B)]
+    parent = [p for n in sizes for p in random_tree(r, n)]
+    run_tree_plan(parent, [n + int(v) for n, v in zip(sizes, r.integers(0, 9, B))], np.cumsum([0] + sizes).tolist(), 2)
+    VerifyCase(sizes, 5, seed=9, near=1.0).check(3)
 
 
 # ------------------------------------------------------------------ together
