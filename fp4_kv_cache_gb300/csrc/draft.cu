@@ -12,7 +12,8 @@ constexpr int kTreeThreads = 128, kMaxNodes = 32 * CSA2D_MAX_WORDS;
 
 // A CTA takes a request, a thread a node: it goes up to the root through the parents in shared memory
 // and writes the mask's words as it leaves them, highest first (parents are lower nodes).  What
-// bounds it is latency: the offsets, the parents, one step a level.
+// bounds it is latency: the offsets, the parents, one step a level (4.1 us for 32 chains of six, 6.2 for
+// four trees of 64).
 __global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const csa2d_tree_args P, uint32_t *d_status)
 {
     __shared__ int32_t s_parent[kMaxNodes];
@@ -80,7 +81,8 @@ constexpr int kMoveThreads = 128, kMoveAhead = 8;
 // A CTA takes a request in one cache, a thread a column of its rows: 16 bytes of codes or a byte of
 // scales, which it moves row by row down the path.  The path rises, so a row is read before anything
 // is written there (path[j] > i for j > i), and no thread touches another's column.  Eight rows are on
-// their way at a time.  Latency bounds it: offsets, path, table, row, store.
+// their way at a time.  Latency bounds it: offsets, path, table, row, store (32 requests in four caches
+// 6.1 us, 64 in twenty 8.2).
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const csa2d_compact_args P, const __grid_constant__ CacheSet set, uint32_t *d_status)
 {
     const PagedView &C = set.c[blockIdx.y];

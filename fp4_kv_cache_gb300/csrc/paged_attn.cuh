@@ -427,8 +427,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *buf, int64_t &
 // FULL: rows of 576 channels with 512 values, so that the chunk counts are constants (windows of 128
 // over MXFP8 147 us, a ragged E4M3-scaled step 964, the chunk 5,917; in the general instance 165, 1,020
 // and 6,052).
-// TREE: the tokens of a request are a tree's nodes, whose rows are the request's last ones; a tile that
-// reaches into those is masked bit by bit.
+// TREE: the tokens of a request are a tree's nodes, whose rows are the request's last ones.  A row tile's
+// keys are the rows before them and then the nodes that its rows see, one behind another; which rows see
+// a key is worked out when the key's row is looked up, two tiles ahead, so that the softmax reads one
+// word.  (All nodes as keys, masked bit by bit in the softmax: 16 trees of up to 25 nodes in a window of 128
+// 51.9 us, now 32.8; four of up to 64 over 16,384 rows 529, now 496; one chain of six with 16 heads over
+// 4,096 rows 26.6, now 24.6; 32 chains over up to 65,536 rows 2,054, as 2,043 before, 662 TFLOP/s.)
 template <int FMT, bool FULL, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ AttnParams P)
 {

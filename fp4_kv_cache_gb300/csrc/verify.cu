@@ -21,6 +21,12 @@
 #include "draft.cuh"
 #include "internal.h"
 
+//
+// What bounds it: each rejection is a pass over a row of the vocabulary that needs the pass before, so the
+// request with most of them sets the time (64 trees of 16 nodes over 131,072 float32 tokens 26.6 us, of
+// which 9.9 are their last rows at the copy rate; half the warps' time is waiting for loads and barriers
+// by profile); one chain of six 10.2 us.  Weights one at a time, with 64-bit bookkeeping of what is not
+// finite, took 35.5 and 12.3.
 namespace csa2 {
 namespace {
 
