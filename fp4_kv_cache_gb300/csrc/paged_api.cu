@@ -1,5 +1,5 @@
 // paged_api.cu -- extern "C" entry points of include/csa2_paged.h: host-side validation before
-// any launch; the kernels live in paged.cu and paged_attn.cu.
+// any launch; the kernels live in paged.cu and paged_attn.cuh.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
