@@ -585,7 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             }
         };
         const int c8 = ((2 * q) ^ key8) << 4;
-        // A block of the product before has left chunks 2 j, 2 j + 1; blocks are done in order.
+        // A block of the product before has left chunks 2 j, 2 j + 1; blocks are done in order.  To be
+        // waited for only while this warp still has something to stage for the tile: after its last signal
+        // the tile's own product may be done too, and the barrier a phase further, which looks like a phase
+        // too few.  (Rows of up to 256 channels: some warps have no task in the second round, or one alone.)
         auto left = [&](uint32_t n, int j) {
             if (n > 0) ok = wait_bar(&M.pv_done[min(j, n_pv - 1)], (n - 1) & 1, &M.abort) && ok;
         };
@@ -650,11 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         auto first_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n) {
             left(n, 0);
             store_tasks(r, One{}, n, 0);
-            left(n, min((w + 2 * kStageWarps) >> 4, pairs - 1));
+            if (live(w + kStageWarps)) left(n, min((w + 2 * kStageWarps) >> 4, pairs - 1));
             store_tasks(r + 1, Two{}, n, 1);
         };
         auto second_round = [&](Raw<FMT, 4> (&r)[3], uint32_t n) {
-            left(n, 3);
+            if (tail || live(w + 3 * kStageWarps)) left(n, 3);
             store_tasks(r, Two{}, n, 3);
             store_tasks(r + 2, One{}, n, 5);
             if (tail) store_tail(n);
