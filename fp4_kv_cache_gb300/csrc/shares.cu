@@ -51,8 +51,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // One CTA: who is forked, which free page each takes, the new lengths; a thread has one of 1,024
 // requests at a time.  What it writes -- lengths and last entries of forked requests -- nobody else
 // reads here: a source is no forked request.  Latency bounds it: source, lengths, last page, scan, page
-// (with the shared pages, and an end of the same requests: 11.8 us for eight forks of 512 pages, 24.6 for
-// 512 of up to 1,024, of which the counts' atomics take most: 32 forks count on the same pages).
+// (with the shared pages, and an end of the same requests: 10.3 us for eight forks of 512 pages).
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     __shared__ int32_t s_warp[kForkThreads / 32];
@@ -103,68 +102,80 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const csa2d_sha
     if (tid == 0) P.n_free[0] = max(n_free - all, 0);
 }
 
-// Table rows are gone through in pieces of a warp's kPiece entries, kAhead a lane, all under way at once,
-// by a kernel of its own: one cluster that did this too was slower however few the pieces (a fork and its
-// end, 9 requests of 512 entries: 13.8 us where these four launches take 11.8; 1,000 of 200: 41 and 16).
-constexpr int kAhead = 8, kPiece = 32 * kAhead;
-__device__ __forceinline__ int32_t pieces(int32_t width) { return (width - 1) / kPiece + 1; }
+// Table rows are gone through by a kernel of its own, a warp for 32 entries of four requests, a lane for an
+// entry of all four: where they hold the same page, as answers to one prompt do, its count is changed once
+// for all of them.  A fork, its copies and end for 16 prompts with 32 answers each and up to 1,024 pages: 22.6
+// us, and 29.5 when a lane had eight entries of one request; 24.6 by groups of 16, 26.6 of 32 (a lane's loads
+// wait for all its requests); without neighbours that share 15.4 and 15.9 (1,000 requests of 200 entries).
+// One cluster that did this and what comes before was slower however few the pieces (the same requests: 41).
+constexpr int kEach = 4, kPagesThreads = 256;
+__device__ __forceinline__ int32_t pieces(int32_t width) { return (width - 1) / 32 + 1; }
 
-// The full pages of forked request b among the entries of a piece.
-__device__ __forceinline__ void fork_pages(const csa2d_share_args &P, const int shift, int b, int32_t piece, uint32_t *d_status)
+// What a warp of the grid has: requests b .. b + 3, entry `at` of this lane.
+struct Piece {
+    int32_t b, at;
+};
+__device__ __forceinline__ Piece piece_of(const csa2d_share_args &P)
 {
-    const int32_t a = P.source[b];
-    if (a < 0 || P.dst[b] == kRefused) return;
-    const int32_t full = P.lens[b] >> shift, n = full - piece * kPiece, lane = threadIdx.x & 31;
-    const int32_t *from = P.block_table + (int64_t)a * P.width + piece * kPiece;
-    int32_t *to = P.block_table + (int64_t)b * P.width + piece * kPiece;
-    int32_t id[kAhead];
+    const int32_t n = pieces(P.width);
+    const int64_t i = (int64_t)blockIdx.x * (kPagesThreads / 32) + threadIdx.x / 32;
+    return {(int32_t)min(i / n * kEach, (int64_t)P.batch), (int32_t)(i % n) * 32 + (int32_t)(threadIdx.x & 31)};
+}
+
+// Adds `by` to the count of each of a lane's pages, once for neighbours that are the same.
+__device__ __forceinline__ void count_pages(const csa2d_share_args &P, const int32_t (&id)[kEach], int32_t by, uint32_t *d_status)
+{
+    int32_t run = 0;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) id[k] = lane + 32 * k < n ? from[lane + 32 * k] : -1;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        if (lane + 32 * k < n) to[lane + 32 * k] = id[k];
+    for (int k = 0; k < kEach; ++k) {
+        run += by;
+        if (k + 1 < kEach && id[k + 1] == id[k]) continue;
         if (id[k] >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        else if (id[k] >= 0) atomicAdd(P.shares + id[k], 1);
+        else if (id[k] >= 0) atomicAdd(P.shares + id[k], run);
+        run = 0;
     }
 }
 
-constexpr int kPagesThreads = 256;
-
+// The full pages of forked requests.
 __global__ void __launch_bounds__(kPagesThreads) page_share_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
-    const int32_t n = pieces(P.width);
-    const int64_t i = (int64_t)blockIdx.x * (kPagesThreads / 32) + threadIdx.x / 32;
-    if (i < (int64_t)P.batch * n) fork_pages(P, shift, (int)(i / n), (int)(i % n), d_status);
+    const Piece w = piece_of(P);
+    const int32_t mine = w.b + (threadIdx.x & 31);             // a lane looks a request up for the warp
+    int32_t source = -1, full = 0;
+    if ((threadIdx.x & 31) < kEach && mine < P.batch) {
+        source = P.source[mine];
+        if (source >= 0 && P.dst[mine] != kRefused) full = P.lens[mine] >> shift;
+    }
+    int32_t id[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int32_t a = __shfl_sync(0xffffffffu, source, k), n = __shfl_sync(0xffffffffu, full, k);
+        id[k] = w.at < n ? P.block_table[(int64_t)a * P.width + w.at] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (w.at < __shfl_sync(0xffffffffu, full, k)) P.block_table[(int64_t)(w.b + k) * P.width + w.at] = id[k];
+    count_pages(P, id, 1, d_status);
 }
 
 // ---------------------------------------------------------------- free
-// The pages of ended request b among the entries of a piece lose a holder each; one without any is
-// marked by a count below 0.
-__device__ __forceinline__ void drop_pages(const csa2d_share_args &P, const int shift, int b, int32_t piece, uint32_t *d_status)
-{
-    if (P.ends[b] == 0) return;
-    const int64_t pages = ((int64_t)max(P.lens[b], 0) + (1 << shift) - 1) >> shift;
-    const int32_t n = (int32_t)min(pages, (int64_t)P.width) - piece * kPiece, lane = threadIdx.x & 31;
-    const int32_t *table = P.block_table + (int64_t)b * P.width + piece * kPiece;
-    int32_t id[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) id[k] = lane + 32 * k < n ? table[lane + 32 * k] : -1;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        if (id[k] >= P.n_pages) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        else if (id[k] >= 0) atomicSub(P.shares + id[k], 1);
-    }
-}
-
+// The pages of ended requests lose a holder each; one without any is marked by a count below 0.
 __global__ void __launch_bounds__(kPagesThreads) page_drop_kernel(const csa2d_share_args P, const int shift, uint32_t *d_status)
 {
     pdl_wait();
     pdl_allow_dependents();
-    const int32_t n = pieces(P.width);
-    const int64_t i = (int64_t)blockIdx.x * (kPagesThreads / 32) + threadIdx.x / 32;
-    if (i < (int64_t)P.batch * n) drop_pages(P, shift, (int)(i / n), (int)(i % n), d_status);
+    const Piece w = piece_of(P);
+    const int32_t mine = w.b + (threadIdx.x & 31);
+    int32_t held = 0;
+    if ((threadIdx.x & 31) < kEach && mine < P.batch && P.ends[mine] != 0)
+        held = (int32_t)min(((int64_t)max(P.lens[mine], 0) + (1 << shift) - 1) >> shift, (int64_t)P.width);
+    int32_t id[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        id[k] = w.at < __shfl_sync(0xffffffffu, held, k) ? P.block_table[(int64_t)(w.b + k) * P.width + w.at] : -1;
+    count_pages(P, id, -1, d_status);
 }
 
 // One cluster: marked pages go on the free list in the order of their ids, so that it does not depend
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
 // CTAs of a warp for each piece of all the table rows.
 unsigned piece_ctas(const csa2d_share_args &a)
 {
-    const int64_t n = (int64_t)a.batch * ((a.width - 1) / kPiece + 1);
+    const int64_t n = ((int64_t)a.batch + kEach - 1) / kEach * ((a.width - 1) / 32 + 1);
     return (unsigned)((n + kPagesThreads / 32 - 1) / (kPagesThreads / 32));
 }
 

@@ -885,6 +885,25 @@ def test_forks_and_ends(B, W, n_pages, page, most, seed):
     assert sorted(P.free) == list(range(n_pages))
 
 
+@pytest.mark.parametrize("W", [3, 33, 70])
+@pytest.mark.parametrize("order", ["one after another", "in turn", "with gaps", "one alone"])
+def test_forks_beside_one_another(W, order):
+    # neighbours that hold the same pages: runs of every length, over and within groups of requests, with
+    # requests between that are refused, end earlier, or hold pages of their own
+    page, P = 2, Pages(23, W, 30 * W, 2)
+    lens = [min(2 * W - 1, 5), 2 * W - 1, 2 * W - 2]
+    P.grow(lens + [0] * 20)
+    source = [-1] * 3 + {"one after another": [0] * 7 + [1] * 9 + [2] * 4, "in turn": [i % 3 for i in range(20)],
+                         "with gaps": [1, 1, -1, 1, 1, 1, 50, 1, 0, 1, 2, 2, 4, 2, -1, -1, 2, 2, 2, 2], "one alone": [-1] * 19 + [1]}[order]
+    P.fork(source)
+    P.grow([0 if n == 0 or n == 2 * W else 1 for n in P.lens])
+    P.same()
+    P.end([int(b % 5 == 4) for b in range(23)])
+    P.end([int(b < 9) for b in range(23)])
+    P.end([1] * 23)
+    assert sorted(P.free) == list(range(30 * W))
+
+
 def test_fork_refusals():
     P = Pages(7, 4, 12, 4)
     P.grow([9, 0, 0, 0, 0, 6, 0])
