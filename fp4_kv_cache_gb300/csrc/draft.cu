@@ -90,16 +90,18 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const csa2d_compa
     pdl_wait();
     pdl_allow_dependents();
     const int32_t keep = P.keep[b];
-    const int64_t n = (int64_t)P.cu[b + 1] - P.cu[b], base = P.lens[b] - n;
-    if (keep == 0) return;
+    const int64_t c0 = P.cu[b], n = P.cu[b + 1] - c0, base = P.lens[b] - n;
     const int32_t *path = P.path + (int64_t)b * P.max_path;
     bool bad = keep < 0 || keep > P.max_path || n < 0 || base < 0;
+    if (P.pos && n > 0) bad |= c0 < 0 || c0 + n > P.n_tokens || P.pos[c0] < 0;      // the plan left it out
     if (!bad)
         for (int i = tid; i < keep; i += kMoveThreads) bad |= path[i] <= (i ? path[i - 1] : -1) || path[i] >= n;
-    if (__syncthreads_or(bad)) {
-        if (blockIdx.y == 0 && tid == 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        return;
+    bad = __syncthreads_or(bad);
+    if (blockIdx.y == 0 && tid == 0) {
+        if (bad && keep != 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
+        if (P.delta) P.delta[b] = n <= 0 || base < 0 ? 0 : (int32_t)((bad ? 0 : keep) - n);
     }
+    if (bad || keep == 0) return;
     const int32_t *table = P.block_table + (int64_t)b * P.width;
     auto slot = [&](int64_t row) -> int32_t {              // -1: in no page
         const int64_t page = row >> C.shift;

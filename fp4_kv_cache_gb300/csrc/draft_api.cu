@@ -102,7 +102,7 @@ csa2_status csa2d_tree_verify(const csa2d_verify_args *a, uint32_t *d_status, cs
     if (a->n_tokens > 0 && (!a->p || !a->token || !a->parent || !a->u)) return CSA2_ERR_INVALID_ARG;
     const size_t value = a->type == CSA2D_F32 ? 4 : 2;
     if (!aligned(a->p, value) || !aligned(a->q, value)) return CSA2_ERR_INVALID_ARG;
-    if (!words(a->token, a->parent, a->cu, a->u, a->r, a->keep, a->path, a->next_token, a->delta, d_status)) return CSA2_ERR_INVALID_ARG;
+    if (!words(a->token, a->parent, a->cu, a->u, a->r, a->keep, a->path, a->next_token, a->delta, a->pos, d_status)) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_tree_verify(*a, d_status, as_stream(stream)));
 }
 
@@ -113,7 +113,8 @@ csa2_status csa2d_compact(const csa2d_compact_args *a, const csa2p_cache *caches
     if (!a || !batch_ok(a->batch) || a->width < 0 || a->max_path < 0 || !cache_set(caches, n, true, set)) return CSA2_ERR_INVALID_ARG;
     if (a->batch == 0 || n == 0) return CSA2_OK;
     if (!a->lens || !a->cu || !a->keep || (a->width > 0 && !a->block_table) || (a->max_path > 0 && !a->path)) return CSA2_ERR_INVALID_ARG;
-    if (!words(a->block_table, a->lens, a->cu, a->path, a->keep, d_status)) return CSA2_ERR_INVALID_ARG;
+    if (a->pos && a->n_tokens < 0) return CSA2_ERR_INVALID_ARG;
+    if (!words(a->block_table, a->lens, a->cu, a->path, a->keep, a->pos, a->delta, d_status)) return CSA2_ERR_INVALID_ARG;
     return from_cuda(launch_compact(*a, set, n, d_status, as_stream(stream)));
 }
 

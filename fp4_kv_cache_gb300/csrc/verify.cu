@@ -166,18 +166,22 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const csa2d_verif
     const T *all_p = static_cast<const T *>(P.p), *all_q = static_cast<const T *>(P.q);
     const int64_t c0 = P.cu[b], n64 = P.cu[b + 1] - c0;
     uint32_t flags = 0;
-    if (n64 <= 0 || c0 < 0 || c0 + n64 > P.n_tokens || n64 > kMaxNodes) {
+    auto leave_out = [&] {
         if (ctas > 1) cluster_wait();
         if (rank > 0) return;
         for (int i = tid; i < P.max_path; i += kThreads) P.path[(int64_t)b * P.max_path + i] = -1;
         if (tid == 0) {
             P.keep[b] = 0;
             P.next_token[b] = -1;
-            P.delta[b] = 0;
+            P.delta[b] = P.pos && n64 > 0 ? -(int32_t)min(n64, (int64_t)INT32_MAX) : 0;
             if (n64 > 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
         }
+    };
+    if (n64 <= 0 || c0 < 0 || c0 + n64 > P.n_tokens || n64 > kMaxNodes) {
+        leave_out();
         return;
     }
+    const int32_t root = P.pos ? P.pos[c0] : 0;           // looked at once the nodes have been read
     const int n = (int)n64;
     if (tid < CSA2D_MAX_WORDS) M.again[tid] = 0u;
     for (int i = tid; i < n; i += kThreads) {
@@ -201,6 +205,10 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const csa2d_verif
         M.u[i] = u;
         M.p[i] = p;
         M.q[i] = q;
+    }
+    if (root < 0) {
+        leave_out();
+        return;
     }
     __syncthreads();
     if (!DRAWN) {

@@ -45,13 +45,13 @@ class VerifyArgs(ctypes.Structure):
     """csa2d_verify_args"""
     _fields_ = [("batch", _I32), ("n_tokens", _I32), ("vocab", _I32), ("type", _I32), ("max_path", _I32), ("p_row", _I64),
                 ("q_row", _I64), ("p", _P), ("q", _P), ("token", _P), ("parent", _P), ("cu", _P), ("u", _P), ("r", _P), ("keep", _P),
-                ("path", _P), ("next_token", _P), ("delta", _P)]
+                ("path", _P), ("next_token", _P), ("delta", _P), ("pos", _P)]
 
 
 class CompactArgs(ctypes.Structure):
     """csa2d_compact_args"""
-    _fields_ = [("batch", _I32), ("width", _I32), ("max_path", _I32), ("block_table", _P), ("lens", _P), ("cu", _P), ("path", _P),
-                ("keep", _P)]
+    _fields_ = [("batch", _I32), ("width", _I32), ("max_path", _I32), ("n_tokens", _I32), ("block_table", _P), ("lens", _P), ("cu", _P),
+                ("path", _P), ("keep", _P), ("pos", _P), ("delta", _P)]
 
 
 class ShareArgs(ctypes.Structure):
@@ -63,8 +63,8 @@ class ShareArgs(ctypes.Structure):
 
 _TREE = struct.Struct("@3i4x5P")                              # csa2d_tree_args
 _ATTN = struct.Struct(_CACHE.format + "7if7P")                # csa2d_tree_attn_args
-_VERIFY = struct.Struct("@5i4x2q11P")                         # csa2d_verify_args
-_COMPACT = struct.Struct("@3i4x5P")                           # csa2d_compact_args
+_VERIFY = struct.Struct("@5i4x2q12P")                         # csa2d_verify_args
+_COMPACT = struct.Struct("@4i7P")                              # csa2d_compact_args
 _SHARE = struct.Struct("@5i4x10P")                            # csa2d_share_args
 
 _ready = None
@@ -177,12 +177,13 @@ def _rows(t, name: str, T: int, V: int, dtype, dev: int):
 
 
 def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = None, d_status=None, stream=None,
-                out: Optional[Verdict] = None) -> Verdict:
+                out: Optional[Verdict] = None, pos=None) -> Verdict:
     """Which drafts stay, and the token behind them.  p [n_tokens, vocab] (float32, float16 or bfloat16;
     rows may be strided): the target's probabilities after each node; q like p: those that each node's
     children were drawn from (None: the drafts are certain); token, parent int32 and u f32 [n_tokens];
     cu int32 [batch + 1]; r f32 [batch]; u and r uniform from 0 to 1.  max_path: entries of a path (None:
-    n_tokens).  See csa2d_tree_verify."""
+    n_tokens).  pos int32 [n_tokens]: tree_plan's, so that requests that it left out keep nothing and give
+    their nodes' rows back.  See csa2d_tree_verify."""
     dev, T, B = p.get_device(), token.numel(), r.numel()
     if p.dtype not in _TYPES or p.dim() != 2:
         raise ValueError("p is float32, float16 or bfloat16 [n_tokens, vocab]")
@@ -200,7 +201,7 @@ def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = No
               _need(out.token, "out.token", _i32, B, dev), _need(out.delta, "out.delta", _i32, B, dev))
     a = _VERIFY.pack(B, T, V, _TYPES[p.dtype], max_path, p_row, q_row, at_p, at_q, _need(token, "token", _i32, T, dev),
                      _need(parent, "parent", _i32, T, dev), _need(cu, "cu", _i32, B + 1, dev), _need(u, "u", _f32, T, dev),
-                     _need(r, "r", _f32, B, dev), *at)
+                     _need(r, "r", _f32, B, dev), *at, _maybe(pos, "pos", _i32, T, dev))
     st = (_ready or _lib()).csa2d_tree_verify(a, _status(d_status, dev), _stream_of(dev, stream))
     if st:
         raise Csa2Error("csa2d_tree_verify", st)
@@ -222,10 +223,11 @@ def _sets(caches: Sequence[PagedCache]):
     return dev, [(b"".join(c.packed for c in part), len(part)) for part in parts]
 
 
-def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, keep, d_status=None, stream=None):
+def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, keep, d_status=None, stream=None, pos=None, delta=None):
     """Rows base + path[b][i] of each request's nodes moved to base + i, i < keep[b], in every cache (base
     = lens[b] - nodes).  block_table int32 [batch, width], lens and keep int32 [batch], cu int32 [batch +
-    1], path int32 [batch, max_path].  See csa2d_compact."""
+    1], path int32 [batch, max_path].  pos int32 [n_tokens]: tree_plan's, so that requests that it left out
+    move nothing; delta int32 [batch]: set to the rows that page_plan has to take back.  See csa2d_compact."""
     dev, sets = _sets(caches)
     B = lens.numel()
     if block_table.dim() != 2 or path.dim() != 2:
@@ -235,8 +237,9 @@ def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, kee
         if c.page != page:
             raise ValueError("the caches have pages of several sizes")
     W, L = block_table.shape[1], path.shape[1]
-    a = _COMPACT.pack(B, W, L, _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
-                      _need(cu, "cu", _i32, B + 1, dev), _need(path, "path", _i32, B * L, dev), _need(keep, "keep", _i32, B, dev))
+    a = _COMPACT.pack(B, W, L, 0 if pos is None else pos.numel(), _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
+                      _need(cu, "cu", _i32, B + 1, dev), _need(path, "path", _i32, B * L, dev), _need(keep, "keep", _i32, B, dev),
+                      _maybe(pos, "pos", _i32, None, dev), _maybe(delta, "delta", _i32, B, dev))
     status, raw = _status(d_status, dev), _stream_of(dev, stream)
     for packed, n in sets:
         st = (_ready or _lib()).csa2d_compact(a, packed, n, status, raw)

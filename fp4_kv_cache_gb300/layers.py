@@ -189,8 +189,12 @@ def draft_layer(cache: "paged.PagedCache", state: PagedState, x: PagedInput, ste
 
 
 def draft_accept(caches, state: PagedState, step: DraftPlan, verdict: "draft.Verdict", d_status=None, stream=None) -> "paged.PagePlan":
-    """The verdict's path becomes the requests' rows in all caches, the other nodes' rows are given back."""
-    draft.paged_compact(caches, state.block_table, state.lens, step.plan.cu, verdict.path, verdict.keep, d_status, stream)
+    """The verdict's path becomes the requests' rows in all caches, the other nodes' rows are given back.  A
+    request that the step's plan left out (more nodes than max_nodes, or nodes past the inputs' rows) has no
+    attention output to be verified from: it is as it was before the step.  tree_verify given step.tree.pos says
+    so too; verdict.delta is set to what is given back."""
+    draft.paged_compact(caches, state.block_table, state.lens, step.plan.cu, verdict.path, verdict.keep, d_status, stream,
+                        step.tree.pos, verdict.delta)
     return paged.page_plan(state.lens, verdict.delta, state.block_table, state.free_pages, state.n_free, caches[0].page, 0,
                            in_place=True, d_status=d_status, stream=stream)
 

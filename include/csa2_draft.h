@@ -125,8 +125,10 @@ CSA2_API csa2_status csa2d_tree_attn(const csa2d_tree_attn_args *a, uint16_t *ou
 /* A draft whose token is outside the vocabulary is passed over (CSA2_DEV_BAD_INDEX).                           */
 /* keep[b] = nodes that stay, node 0 among them; path[b] = these nodes in order, -1 behind them;                 */
 /* next_token[b] = the token drawn (-1 where p_v has no weight: CSA2D_DEV_NO_TOKEN); delta[b] = keep[b] - n.      */
-/* A path of max_path nodes ends there.  A request without nodes gets keep 0, token -1, delta 0; so does one       */
-/* with nodes outside 0..n_tokens, or more than 32 CSA2D_MAX_WORDS of them (CSA2_DEV_BAD_INDEX).                     */
+/* A path of max_path nodes ends there.  A request without nodes gets keep 0, token -1, delta 0.  One with nodes   */
+/* outside 0..n_tokens, with more than 32 CSA2D_MAX_WORDS of them, or, where pos is given, that csa2d_tree_plan      */
+/* left out (its node 0 has a pos below 0: csa2d_tree_attn leaves its outputs as they were, so there is nothing to    */
+/* verify) gets keep 0 and token -1 too (CSA2_DEV_BAD_INDEX); its delta is -n where pos is given, else 0.               */
 /* ---------------------------------------------------------------------------------- */
 typedef enum { CSA2D_F32 = 0, CSA2D_F16 = 1, CSA2D_BF16 = 2 } csa2d_float;
 typedef struct {
@@ -147,6 +149,7 @@ typedef struct {
     int32_t *path;            /* [batch, max_path]                                               */
     int32_t *next_token;      /* [batch]                                                         */
     int32_t *delta;           /* [batch]                                                         */
+    const int32_t *pos;       /* [n_tokens] csa2d_tree_plan's, or NULL                           */
 } csa2d_verify_args;
 CSA2_API csa2_status csa2d_tree_verify(const csa2d_verify_args *a, uint32_t *d_status, csa2_stream stream);
 
@@ -155,20 +158,27 @@ CSA2_API csa2_status csa2d_tree_verify(const csa2d_verify_args *a, uint32_t *d_s
 /* row base + path[b][i] of request b goes, as it is stored, to row base + i, i < keep[b]; other rows   */
 /* stay as they are.  A path has to rise and stay below n: a request whose path does not, or whose keep   */
 /* is outside 0..max_path, moves nothing; neither does one with fewer rows than nodes (CSA2_DEV_BAD_INDEX   */
-/* each).  A row whose page is none, at either end, is not moved (CSA2_DEV_BAD_INDEX).  Caches must not       */
-/* share memory, and no page may be held by two requests at rows that move.                                   */
+/* each).  Where pos is given, neither does one whose nodes are not all in 0..n_tokens or whose node 0 has a  */
+/* pos below 0: csa2d_tree_plan left it out, whatever its keep (CSA2_DEV_BAD_INDEX where that is not 0).       */
+/* A row whose page is none, at either end, is not moved (CSA2_DEV_BAD_INDEX).  Caches must not share         */
+/* memory, and no page may be held by two requests at rows that move.                                         */
+/* delta[b], where it is given: keep[b] - n for a request whose path was taken, -n for one with nodes that     */
+/* moves nothing (its nodes' rows all go back), 0 for one without nodes or with fewer rows than nodes.         */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;            /* requests, 0..CSA2P_MAX_BATCH                                    */
     int32_t width;            /* block table entries a request                                   */
     int32_t max_path;         /* entries of a path                                               */
+    int32_t n_tokens;         /* entries of pos                                                  */
     const int32_t *block_table; /* [batch, width]                                                */
     const int32_t *lens;      /* [batch] rows held, the nodes' included                          */
     const int32_t *cu;        /* [batch + 1]: n = cu[b+1] - cu[b] nodes                          */
     const int32_t *path;      /* [batch, max_path]                                               */
     const int32_t *keep;      /* [batch]                                                         */
+    const int32_t *pos;       /* [n_tokens] csa2d_tree_plan's, or NULL                           */
+    int32_t *delta;           /* [batch] out, or NULL                                            */
 } csa2d_compact_args;
-/* caches: n of them in host memory, 0..CSA2D_MAX_CACHES, with one page size.                     */
+/* caches: n of them in host memory, 0..CSA2D_MAX_CACHES, with one page size (0: nothing is done). */
 CSA2_API csa2_status csa2d_compact(const csa2d_compact_args *a, const csa2p_cache *caches, int32_t n,
                                    uint32_t *d_status, csa2_stream stream);
 
