@@ -182,13 +182,13 @@ def tree_verify(p, token, parent, cu, u, r, q=None, max_path: Optional[int] = No
     rows may be strided): the target's probabilities after each node; q like p: those that each node's
     children were drawn from (None: the drafts are certain); token, parent int32 and u f32 [n_tokens];
     cu int32 [batch + 1]; r f32 [batch]; u and r uniform from 0 to 1.  max_path: entries of a path (None:
-    n_tokens).  pos int32 [n_tokens]: tree_plan's, so that requests that it left out keep nothing and give
+    n_tokens, at most the 1,024 nodes that a request may have; the trees' largest depth + 1 is enough).  pos int32 [n_tokens]: tree_plan's, so that requests that it left out keep nothing and give
     their nodes' rows back.  See csa2d_tree_verify."""
     dev, T, B = p.get_device(), token.numel(), r.numel()
     if p.dtype not in _TYPES or p.dim() != 2:
         raise ValueError("p is float32, float16 or bfloat16 [n_tokens, vocab]")
     V = p.shape[1]
-    max_path = max(T, 1) if max_path is None else max_path
+    max_path = min(max(T, 1), 32 * MAX_WORDS) if max_path is None else max_path
     at_p, p_row = _rows(p, "p", T, V, p.dtype, dev)
     at_q, q_row = (0, V) if q is None else _rows(q, "q", T, V, p.dtype, dev)
     if out is None:
