@@ -171,7 +171,7 @@ class Verdict:
 
 def _rows(t, name: str, T: int, V: int, dtype, dev: int):
     """Address and row stride of probabilities [T, V]."""
-    if t.dim() != 2 or t.shape != (T, V) or t.dtype is not dtype or t.get_device() != dev or dev < 0 or (V > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or t.shape != (T, V) or t.dtype is not dtype or t.get_device() != dev or dev < 0 or (T > 0 and V > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be {dtype} [{T}, {V}] on the GPU with contiguous rows, not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr(), t.stride(0) if T > 1 else V
 

@@ -27,3 +27,14 @@ def test_many_requests_take_little():
     v = draft.tree_verify(*args, q=None)
     assert torch.cuda.max_memory_allocated() - before <= 4000 * 1024 * 4 + 4 * 4000 * 4 + 8192
     assert v.keep.tolist() == [1] * 4000
+
+
+def test_a_call_without_tokens_takes_probabilities_of_any_stride():
+    # rows that are not there have no layout
+    i, f = (lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)), (lambda n: torch.zeros(n, device=DEV))
+    for p in (torch.empty((0, 8), device=DEV), torch.empty_strided((0, 8), (1, 0), device=DEV), torch.empty((8, 0), device=DEV).T):
+        for q in (None, p):
+            v = draft.tree_verify(p, i(0), i(0), i(3), f(0), f(2), q=q)
+            assert v.keep.tolist() == v.delta.tolist() == [0, 0] and v.token.tolist() == [-1, -1] and v.path.tolist() == [[-1], [-1]]
+    with pytest.raises(ValueError):
+        draft.tree_verify(torch.rand((8, 3), device=DEV).T, i(3), i(3), ints([0, 3]), f(3), f(1))
