@@ -192,7 +192,7 @@ def draft_accept(caches, state: PagedState, step: DraftPlan, verdict: "draft.Ver
     """The verdict's path becomes the requests' rows in all caches, the other nodes' rows are given back.  A
     request that the step's plan left out (more nodes than max_nodes, or nodes past the inputs' rows) has no
     attention output to be verified from: it is as it was before the step.  tree_verify given step.tree.pos says
-    so too; verdict.delta is set to what is given back."""
+    so too; else verdict.delta is lowered to that."""
     draft.paged_compact(caches, state.block_table, state.lens, step.plan.cu, verdict.path, verdict.keep, d_status, stream,
                         step.tree.pos, verdict.delta)
     return paged.page_plan(state.lens, verdict.delta, state.block_table, state.free_pages, state.n_free, caches[0].page, 0,

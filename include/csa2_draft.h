@@ -162,8 +162,9 @@ CSA2_API csa2_status csa2d_tree_verify(const csa2d_verify_args *a, uint32_t *d_s
 /* pos below 0: csa2d_tree_plan left it out, whatever its keep (CSA2_DEV_BAD_INDEX where that is not 0).       */
 /* A row whose page is none, at either end, is not moved (CSA2_DEV_BAD_INDEX).  Caches must not share         */
 /* memory, and no page may be held by two requests at rows that move.                                         */
-/* delta[b], where it is given: keep[b] - n for a request whose path was taken, -n for one with nodes that     */
-/* moves nothing (its nodes' rows all go back), 0 for one without nodes or with fewer rows than nodes.         */
+/* delta, where it is given, is what csa2p_page_plan will add to lens (csa2d_tree_verify's): that of a request  */
+/* that keeps nothing, is left out or whose path is refused is lowered to -n, so that its nodes' rows all go     */
+/* back; others, and those with fewer rows than nodes, stay as they are.                                          */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;            /* requests, 0..CSA2P_MAX_BATCH                                    */
@@ -176,7 +177,7 @@ typedef struct {
     const int32_t *path;      /* [batch, max_path]                                               */
     const int32_t *keep;      /* [batch]                                                         */
     const int32_t *pos;       /* [n_tokens] csa2d_tree_plan's, or NULL                           */
-    int32_t *delta;           /* [batch] out, or NULL                                            */
+    int32_t *delta;           /* [batch] in and out, or NULL                                     */
 } csa2d_compact_args;
 /* caches: n of them in host memory, 0..CSA2D_MAX_CACHES, with one page size (0: nothing is done). */
 CSA2_API csa2_status csa2d_compact(const csa2d_compact_args *a, const csa2p_cache *caches, int32_t n,

@@ -64,9 +64,10 @@ def test_compact_gives_back_what_does_not_move():
     n_tokens = cu[10]                                                       # the last request's nodes are not all there
     pos = ints([7] * n_tokens)
     pos[cu[1]:cu[2]] = -1
-    want_delta = [-15, -20, -20, -20, -20, -20, -20, 0, 0, -17, -20]
+    delta0 = [-15, -15, 3, -30, -20, -19, 0, 7, -3, -30, -17]                # (-30: the request ends, whatever stays)
+    want_delta = [-15, -20, -20, -30, -20, -20, -20, 7, -3, -30, -20]
     for caches in ([bytes_cache(n_pages, page, 64, paged.MXFP4, 5)], [bytes_cache(n_pages, page, 32, paged.BF16, i) for i in range(35)]):
-        before, st, delta = [raw(c) for c in caches], status(), ints([99] * 11)
+        before, st, delta = [raw(c) for c in caches], status(), ints(delta0)
         draft.paged_compact(caches, ints(table), ints(lens), ints(cu), ints(path), ints(keep), d_status=st, pos=pos, delta=delta)
         moved = list(keep)
         moved[1] = moved[10] = 0
@@ -79,12 +80,12 @@ def test_compact_gives_back_what_does_not_move():
 def test_compact_delta_alone():
     # without pos nothing is left out; a request that keeps nothing is no mistake
     page, table = 8, np.array([[0, 1], [2, 3], [4, 5]])
-    cache, st, delta = bytes_cache(6, page, 64, paged.MXFP8, 5), status(), ints([99] * 3)
+    cache, st, delta = bytes_cache(6, page, 64, paged.MXFP8, 5), status(), ints([-4, 0, 5])
     want = raw(cache)
     args = (table, [14, 16, 9], [0, 6, 10, 10], np.array([[0, 2], [-1, -1], [-1, -1]]), [2, 0, 0])
     compact_ref(want, *args, page, 6)
     draft.paged_compact([cache], *(ints(a) for a in args), d_status=st, delta=delta)
-    assert int(st) == 0 and delta.tolist() == [-4, -4, 0] and all(np.array_equal(a, b) for a, b in zip(raw(cache), want))
+    assert int(st) == 0 and delta.tolist() == [-4, -4, 5] and all(np.array_equal(a, b) for a, b in zip(raw(cache), want))
 
 
 # ------------------------------------------------------------------ together
@@ -139,3 +140,17 @@ def test_a_step_leaves_out_what_its_plan_left_out(case, given):
     for c, rows in zip(caches, old):
         for x, y in zip(raw(c), rows):
             assert np.array_equal(x[state.block_table[bad, :held[bad]].cpu().numpy()].reshape(-1, x.shape[2])[:before[bad]], y)
+
+
+def test_a_request_that_ends_with_its_step():
+    # the server gives a delta of its own: the request's rows all go, its path is moved or not
+    page, H, d, B, g = 16, 4, 64, 2, torch.Generator(device=DEV).manual_seed(4)
+    cache, state = paged.PagedCache.new(30, page, d), layers.PagedState(ints([0] * B), ints(np.full((B, 10), -1)), ints(range(30)), ints([30]))
+    x = lambda delta: layers.PagedInput(torch.randn((sum(delta), H, d), generator=g, device=DEV).bfloat16(),  # noqa: E731
+                                        torch.randn((sum(delta), d), generator=g, device=DEV).bfloat16(), ints(delta))
+    layers.paged_layer(cache, state, x([40, 20]), 0, d)
+    step = layers.draft_plan(page, state, x([4, 4]), ints([-1, 0, 1, 0] * 2), 4)
+    v = draft.Verdict(ints([2, 2]), ints([[0, 3], [0, 3]]), ints([1, 1]), ints([-44, -2]))
+    st = status()
+    layers.draft_accept([cache], state, step, v, d_status=st)
+    assert int(st) == 0 and state.lens.tolist() == [0, 22] and int(state.n_free) == 28 and v.delta.tolist() == [-44, -2]
