@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const csa2d_compa
     bad = __syncthreads_or(bad);
     if (blockIdx.y == 0 && tid == 0) {
         if (bad && keep != 0) dev_flag(d_status, CSA2_DEV_BAD_INDEX);
-        if (P.delta && (bad || keep == 0) && n > 0 && base >= 0) P.delta[b] = min(P.delta[b], (int32_t)-n);
+        if (P.delta && bad && n > 0 && base >= 0) P.delta[b] = min(P.delta[b], (int32_t)-n);
     }
     if (bad || keep == 0) return;
     const int32_t *table = P.block_table + (int64_t)b * P.width;

@@ -227,8 +227,8 @@ def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, kee
     """Rows base + path[b][i] of each request's nodes moved to base + i, i < keep[b], in every cache (base
     = lens[b] - nodes).  block_table int32 [batch, width], lens and keep int32 [batch], cu int32 [batch +
     1], path int32 [batch, max_path].  pos int32 [n_tokens]: tree_plan's, so that requests that it left out
-    move nothing; delta int32 [batch]: tree_verify's, lowered to take all nodes' rows back where nothing is
-    kept or moved.  See csa2d_compact."""
+    move nothing; delta int32 [batch]: tree_verify's, lowered to take all nodes' rows back where a
+    request is left out or its path is refused.  See csa2d_compact."""
     dev, sets = _sets(caches)
     B = lens.numel()
     if block_table.dim() != 2 or path.dim() != 2:

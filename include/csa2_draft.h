@@ -163,8 +163,8 @@ CSA2_API csa2_status csa2d_tree_verify(const csa2d_verify_args *a, uint32_t *d_s
 /* A row whose page is none, at either end, is not moved (CSA2_DEV_BAD_INDEX).  Caches must not share         */
 /* memory, and no page may be held by two requests at rows that move.                                         */
 /* delta, where it is given, is what csa2p_page_plan will add to lens (csa2d_tree_verify's): that of a request  */
-/* that keeps nothing, is left out or whose path is refused is lowered to -n, so that its nodes' rows all go     */
-/* back; others, and those with fewer rows than nodes, stay as they are.                                          */
+/* that is left out by pos or whose path is refused is lowered to -n, so that its nodes' rows all go back;       */
+/* others, and those with fewer rows than nodes, stay as they are.                                                */
 /* ---------------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;            /* requests, 0..CSA2P_MAX_BATCH                                    */

@@ -64,8 +64,8 @@ def test_compact_gives_back_what_does_not_move():
     n_tokens = cu[10]                                                       # the last request's nodes are not all there
     pos = ints([7] * n_tokens)
     pos[cu[1]:cu[2]] = -1
-    delta0 = [-15, -15, 3, -30, -20, -19, 0, 7, -3, -30, -17]                # (-30: the request ends, whatever stays)
-    want_delta = [-15, -20, -20, -30, -20, -20, -20, 7, -3, -30, -20]
+    delta0 = [-15, -15, 3, -30, -20, -19, 0, 7, -3, -30, -17]               # (-30: the request ends, whatever stays)
+    want_delta = [-15, -20, -20, -30, -20, -20, 0, 7, -3, -30, -20]
     for caches in ([bytes_cache(n_pages, page, 64, paged.MXFP4, 5)], [bytes_cache(n_pages, page, 32, paged.BF16, i) for i in range(35)]):
         before, st, delta = [raw(c) for c in caches], status(), ints(delta0)
         draft.paged_compact(caches, ints(table), ints(lens), ints(cu), ints(path), ints(keep), d_status=st, pos=pos, delta=delta)
@@ -78,14 +78,14 @@ def test_compact_gives_back_what_does_not_move():
 
 
 def test_compact_delta_alone():
-    # without pos nothing is left out; a request that keeps nothing is no mistake
+    # without pos nothing is left out; a request that keeps nothing is no mistake: its delta is the server's
     page, table = 8, np.array([[0, 1], [2, 3], [4, 5]])
     cache, st, delta = bytes_cache(6, page, 64, paged.MXFP8, 5), status(), ints([-4, 0, 5])
     want = raw(cache)
     args = (table, [14, 16, 9], [0, 6, 10, 10], np.array([[0, 2], [-1, -1], [-1, -1]]), [2, 0, 0])
     compact_ref(want, *args, page, 6)
     draft.paged_compact([cache], *(ints(a) for a in args), d_status=st, delta=delta)
-    assert int(st) == 0 and delta.tolist() == [-4, -4, 5] and all(np.array_equal(a, b) for a, b in zip(raw(cache), want))
+    assert int(st) == 0 and delta.tolist() == [-4, 0, 5] and all(np.array_equal(a, b) for a, b in zip(raw(cache), want))
 
 
 # ------------------------------------------------------------------ together
