@@ -13,7 +13,7 @@ constexpr int kTreeThreads = 128, kMaxNodes = 32 * CSA2D_MAX_WORDS;
 // A CTA takes a request, a thread a node: it goes up to the root through the parents in shared memory
 // and writes the mask's words as it leaves them, highest first (parents are lower nodes).  What
 // bounds it is latency: the offsets, the parents, one step a level (4.1 us for 32 chains of six, 6.2 for
-// four trees of 64).
+// four trees of up to 64).
 __global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const csa2d_tree_args P, uint32_t *d_status)
 {
     __shared__ int32_t s_parent[kMaxNodes];

@@ -259,7 +259,10 @@ __device__ __forceinline__ int32_t tree_low(const AttnParams &P, int32_t t, int3
     return (int32_t)lo;                                    // positions are below 2^31
 }
 // Word w of the nodes that some row of a row tile sees, from the masks of its tokens t0 .. t1.  Beyond
-// kUnion words in all, every node counts: looking for less would take longer than their keys.
+// kUnion words in all, every node counts: looking for less takes longer than their keys (plan and attention
+// of eight trees of 128 nodes over 1,024 rows of MXFP4, 576 / 512, with and without looking: 4 heads, 64
+// words a tile, 63 and 47 us; 8 heads, 32 words, 74 and 68; 16 heads, 16 or 20 words, 112 and 105; 64
+// heads, four words, 306 and 307, and in a window of 128 103 and 130).
 constexpr int kUnion = 32;
 __device__ __forceinline__ uint32_t tree_union(const AttnParams &P, int32_t t0, int32_t t1, int32_t tokens, int w)
 {
@@ -390,7 +393,7 @@ struct Misc : TreeMisc<TREE> {
     alignas(16) int32_t lo[4][kRows], hi[4][kRows];      // keys that a row sees, by row tile (not of trees)
     int64_t scan[kThreads / 32];
     int64_t item_unit;                  // first unit of this CTA's first item
-    Walk<TREE> walk[4];                       // of the upper half's warps: two tiles ahead
+    Walk<TREE> walk[4];                 // of the upper half's warps: two tiles ahead
     uint32_t nan[2][4];                 // keys with a value that is not finite
     int32_t b, j, off;
     uint32_t tmem;
@@ -431,8 +434,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *buf, int64_t &
 // keys are the rows before them and then the nodes that its rows see, one behind another; which rows see
 // a key is worked out when the key's row is looked up, two tiles ahead, so that the softmax reads one
 // word.  (All nodes as keys, masked bit by bit in the softmax: 16 trees of up to 25 nodes in a window of 128
-// 51.9 us, now 32.8; four of up to 64 over 16,384 rows 529, now 496; one chain of six with 16 heads over
-// 4,096 rows 26.6, now 24.6; 32 chains over up to 65,536 rows 2,054, as 2,043 before, 662 TFLOP/s.)
+// 51.9 us, now 32.8; four of up to 64 over 16,384 rows 529, now 496 to 503; one chain of six with 16 heads
+// over 4,096 rows 26.6, now 24.6; 32 chains over up to 65,536 rows 2,054 to 2,068, as 2,043 before, 655 to 659
+// TFLOP/s.  The attention's two launches alone, replayed: without the plan of the trees, 4 to 6 us.)
 template <int FMT, bool FULL, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ AttnParams P)
 {
@@ -940,22 +944,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     }
                 } else {
 #pragma unroll 1
-                for (int c0 = 0; c0 < 32; c0 += 16) {
-                    uint32_t r[16];
-                    tc::tc_ld_32x32b_x16(lane_t + c0, r);
-                    tc::tc_wait_ld();
+                    for (int c0 = 0; c0 < 32; c0 += 16) {
+                        uint32_t r[16];
+                        tc::tc_ld_32x32b_x16(lane_t + c0, r);
+                        tc::tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const int4 lo = *reinterpret_cast<const int4 *>(&M.lo[item][c_lo + c0 + c]);
-                        const int4 hi = *reinterpret_cast<const int4 *>(&M.hi[item][c_lo + c0 + c]);
-                        auto seen = [&](uint32_t x, int l, int h) { return !(have && key >= l && key < h) ? 0xff800000u : nan ? 0x7fc00000u : x; };
-                        r[c] = seen(r[c], lo.x, hi.x);
-                        r[c + 1] = seen(r[c + 1], lo.y, hi.y);
-                        r[c + 2] = seen(r[c + 2], lo.z, hi.z);
-                        r[c + 3] = seen(r[c + 3], lo.w, hi.w);
+                        for (int c = 0; c < 16; c += 4) {
+                            const int4 lo = *reinterpret_cast<const int4 *>(&M.lo[item][c_lo + c0 + c]);
+                            const int4 hi = *reinterpret_cast<const int4 *>(&M.hi[item][c_lo + c0 + c]);
+                            auto seen = [&](uint32_t x, int l, int h) { return !(have && key >= l && key < h) ? 0xff800000u : nan ? 0x7fc00000u : x; };
+                            r[c] = seen(r[c], lo.x, hi.x);
+                            r[c + 1] = seen(r[c + 1], lo.y, hi.y);
+                            r[c + 2] = seen(r[c + 2], lo.z, hi.z);
+                            r[c + 3] = seen(r[c + 3], lo.w, hi.w);
+                        }
+                        tc::tc_st_32x32b_x16(lane_t + c0, r);
                     }
-                    tc::tc_st_32x32b_x16(lane_t + c0, r);
-                }
                 }
                 tc::tc_wait_st();
             }

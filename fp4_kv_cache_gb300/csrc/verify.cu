@@ -14,6 +14,14 @@
 // even, since h 2^20 is even.  Two weights go through this at a time (add, multiply and fma of two
 // floats are one instruction here); what has to be looked at one by one -- values below 0, above 1 or
 // not finite -- is found by the largest bit pattern of a load.
+//
+// What bounds it: each rejection is a pass over a row of the vocabulary that needs the pass before, so the
+// request with most of them sets the time (64 trees of up to 16 nodes over 131,072 float32 tokens 26.6 us, of
+// which 9.9 are their last rows at the copy rate; half the warps' time is waiting for loads and barriers
+// by profile); one chain of six 10.2 us.  Behind the last pass one warp looks for the token, a load, a scan
+// and a branch at a time through its run: the same calls with r = 0, where the first turn finds it, take 22.0 and
+// 9.8 us, with r = 1, where the last one does, 28.7 and 12.3.  Weights one at a time, with 64-bit bookkeeping
+// of what is not finite, took 35.5 and 12.3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,12 +29,6 @@
 #include "draft.cuh"
 #include "internal.h"
 
-//
-// What bounds it: each rejection is a pass over a row of the vocabulary that needs the pass before, so the
-// request with most of them sets the time (64 trees of 16 nodes over 131,072 float32 tokens 26.6 us, of
-// which 9.9 are their last rows at the copy rate; half the warps' time is waiting for loads and barriers
-// by profile); one chain of six 10.2 us.  Weights one at a time, with 64-bit bookkeeping of what is not
-// finite, took 35.5 and 12.3.
 namespace csa2 {
 namespace {
 
@@ -465,8 +467,10 @@ cudaError_t launch(const csa2d_verify_args &a, int ctas, uint32_t *d_status, cud
 cudaError_t launch_tree_verify(const csa2d_verify_args &a, uint32_t *d_status, cudaStream_t s)
 {
     // CTAs a request: a power of two of them, while all requests' fit the GPU at once (two an SM; 64 trees
-    // of 16 nodes over 131,072 tokens: 26.6 us with four, 28.8 with eight, 41 with two; one chain of six:
-    // 10.2 us with eight, 14.4 with four) and each has a few thousand tokens.
+    // of up to 16 nodes over 131,072 tokens: 26.6 us with four, 28.8 with eight, 41 with two; one chain of six:
+    // 10.2 us with eight, 14.4 with four) and each has a few thousand tokens.  CTAs of 256 threads, four an SM
+    // and so eight a request of that batch, take 24.4 us for it, but 14.4 for the chain and 16.4 where this
+    // takes 14.3 (33 trees over 32,003 bf16 tokens); both sizes would be twice the instances.
     int ctas = kMaxCtas;
     while (ctas > 1 && ((int64_t)a.batch * ctas > 2 * (int64_t)device_sm_count() || a.vocab < 2048 * ctas)) ctas /= 2;
     switch (a.type) {

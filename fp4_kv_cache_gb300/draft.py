@@ -272,7 +272,8 @@ def page_fork(source, lens, block_table, shares, free_pages, n_free, page: int, 
               out: Optional[Fork] = None) -> Fork:
     """Requests with source[b] >= 0 take over that request's rows: lens, block_table, shares (int32
     [n_pages], a page's holders beyond the first) and n_free are updated, and the pages to copy are
-    returned.  See csa2d_page_fork."""
+    returned.  From then on such requests end with page_free: page_plan gives pages back without looking at
+    shares, so it may take rows of them back only down to the length at the fork.  See csa2d_page_fork."""
     B, dev = lens.numel(), lens.get_device()
     if out is None:
         device = lens.device

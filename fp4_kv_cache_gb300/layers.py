@@ -113,7 +113,7 @@ class PagedInput:
     """One step's new tokens, requests one after another: queries, cache rows, and how many of each."""
     q: torch.Tensor             # bf16 [T, H, d], not rotated
     x: torch.Tensor             # bf16 [T, d] cache rows, not rotated
-    delta: torch.Tensor         # int32 [B] rows added (or, below 0, taken back)
+    delta: torch.Tensor         # int32 [B] rows added (or, below 0, taken back: not of pages that requests share)
     cos_sin: Optional[torch.Tensor] = None      # f32 [n_pos, rope_dim]; None: no rotation
     pos: Optional[torch.Tensor] = None          # int32 [axes, T]; None: each row's position in its request
     sections: Optional[tuple] = None            # pairs of each axis
@@ -167,7 +167,9 @@ class DraftPlan:
 def draft_plan(page: int, state: PagedState, x: PagedInput, parent: torch.Tensor, max_nodes: int, d_status=None,
                stream=None) -> DraftPlan:
     """A step's new tokens are trees: slots for all nodes (x.delta of each request), their positions and
-    masks.  parent int32 [T]: the node that each follows, counted from its request's first, or -1."""
+    masks.  parent int32 [T]: the node that each follows, counted from its request's first, or -1.  A request
+    with more than max_nodes nodes (rounded up to whole words of 32), or with nodes past x's rows, is left out of the
+    step (DEV_BAD_INDEX): its positions are -1, its outputs are not written, and draft_accept takes its nodes back."""
     T = x.q.shape[0]
     plan = paged.page_plan(state.lens, x.delta, state.block_table, state.free_pages, state.n_free, page, T,
                            in_place=True, d_status=d_status, stream=stream)

@@ -11,9 +11,12 @@
  *   csa2d_tree_attn     attention of the nodes over their requests' pages
  *   csa2d_tree_verify   which path of nodes stays, and the token behind it
  *   csa2d_compact       the path's rows moved together, in every layer's cache
- *   csa2p_page_plan     the other nodes' rows given back (delta = rows kept - nodes)
+ *   csa2p_page_plan     the other nodes' rows given back (delta, as csa2d_compact left it)
  *
- * and requests that continue one prompt in several ways share its pages:
+ * A request that csa2d_tree_plan leaves out has pos -1 throughout; verification and compaction take pos,
+ * so that it keeps nothing and its nodes' rows all go back.
+ *
+ * Requests that continue one prompt in several ways share its pages:
  *
  *   csa2d_page_fork     block tables, page counts and lengths of the forked requests
  *   csa2d_page_copy     the contents of pages, in every layer's cache
@@ -118,9 +121,12 @@ CSA2_API csa2_status csa2d_tree_attn(const csa2d_tree_attn_args *a, uint16_t *ou
 /* where nothing is left): the lowest y with                                                              */
 /*   sum_{x <= y} w(x) > floor(W M / 2^24),  W = sum w,  M = floor(r 2^24) held to 0..2^24-1               */
 /* where w(x) is the weight as a whole number of 2^-40, the nearest, ties to even, held to 2^40.            */
-/* So the kept tokens and the next are distributed as the target's own.  Every float32 operation above is    */
-/* rounded once, in the order written; sums are of whole numbers w(x) (m is their sum x 2^-40, rounded to     */
-/* float32): the same inputs give the same tokens whatever the order.                                         */
+/* So, where the rows of p and q sum to 1 and u and r are uniform, the kept tokens and the next are            */
+/* distributed as the target's own, to within the numbers' steps: r counts as one of 2^24, so the chance of     */
+/* each next token is less than 2^-24 off w / W (one lighter than W 2^-24 has none or 2^-24; over a flat tail    */
+/* of 2^18 tokens this adds up to 1.6% at most).  Every float32 operation above is rounded once, in the order     */
+/* written; sums are of whole numbers w(x) (m is their sum x 2^-40, rounded to float32): the same inputs give     */
+/* the same tokens whatever the order.                                                                            */
 /* Values of p and q below 0 or not finite count as 0 and set CSA2_DEV_NONFINITE where they are used.          */
 /* A draft whose token is outside the vocabulary is passed over (CSA2_DEV_BAD_INDEX).                           */
 /* keep[b] = nodes that stay, node 0 among them; path[b] = these nodes in order, -1 behind them;                 */
