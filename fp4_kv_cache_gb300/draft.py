@@ -50,8 +50,8 @@ class VerifyArgs(ctypes.Structure):
 
 class CompactArgs(ctypes.Structure):
     """csa2d_compact_args"""
-    _fields_ = [("batch", _I32), ("width", _I32), ("max_path", _I32), ("n_tokens", _I32), ("block_table", _P), ("lens", _P), ("cu", _P),
-                ("path", _P), ("keep", _P), ("pos", _P), ("delta", _P)]
+    _fields_ = [("batch", _I32), ("width", _I32), ("max_path", _I32), ("block_table", _P), ("lens", _P), ("cu", _P), ("path", _P),
+                ("keep", _P), ("pos", _P), ("delta", _P), ("n_tokens", _I32)]
 
 
 class ShareArgs(ctypes.Structure):
@@ -64,7 +64,7 @@ class ShareArgs(ctypes.Structure):
 _TREE = struct.Struct("@3i4x5P")                              # csa2d_tree_args
 _ATTN = struct.Struct(_CACHE.format + "7if7P")                # csa2d_tree_attn_args
 _VERIFY = struct.Struct("@5i4x2q12P")                         # csa2d_verify_args
-_COMPACT = struct.Struct("@4i7P")                              # csa2d_compact_args
+_COMPACT = struct.Struct("@3i4x7Pi4x")                        # csa2d_compact_args
 _SHARE = struct.Struct("@5i4x10P")                            # csa2d_share_args
 
 _ready = None
@@ -238,9 +238,9 @@ def paged_compact(caches: Sequence[PagedCache], block_table, lens, cu, path, kee
         if c.page != page:
             raise ValueError("the caches have pages of several sizes")
     W, L = block_table.shape[1], path.shape[1]
-    a = _COMPACT.pack(B, W, L, 0 if pos is None else pos.numel(), _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
+    a = _COMPACT.pack(B, W, L, _need(block_table, "block_table", _i32, B * W, dev), _need(lens, "lens", _i32, B, dev),
                       _need(cu, "cu", _i32, B + 1, dev), _need(path, "path", _i32, B * L, dev), _need(keep, "keep", _i32, B, dev),
-                      _maybe(pos, "pos", _i32, None, dev), _maybe(delta, "delta", _i32, B, dev))
+                      _maybe(pos, "pos", _i32, None, dev), _maybe(delta, "delta", _i32, B, dev), 0 if pos is None else pos.numel())
     status, raw = _status(d_status, dev), _stream_of(dev, stream)
     for packed, n in sets:
         st = (_ready or _lib()).csa2d_compact(a, packed, n, status, raw)

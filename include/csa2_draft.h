@@ -176,7 +176,6 @@ typedef struct {
     int32_t batch;            /* requests, 0..CSA2P_MAX_BATCH                                    */
     int32_t width;            /* block table entries a request                                   */
     int32_t max_path;         /* entries of a path                                               */
-    int32_t n_tokens;         /* entries of pos                                                  */
     const int32_t *block_table; /* [batch, width]                                                */
     const int32_t *lens;      /* [batch] rows held, the nodes' included                          */
     const int32_t *cu;        /* [batch + 1]: n = cu[b+1] - cu[b] nodes                          */
@@ -184,6 +183,7 @@ typedef struct {
     const int32_t *keep;      /* [batch]                                                         */
     const int32_t *pos;       /* [n_tokens] csa2d_tree_plan's, or NULL                           */
     int32_t *delta;           /* [batch] in and out, or NULL                                     */
+    int32_t n_tokens;         /* entries of pos                                                  */
 } csa2d_compact_args;
 /* caches: n of them in host memory, 0..CSA2D_MAX_CACHES, with one page size (0: nothing is done). */
 CSA2_API csa2_status csa2d_compact(const csa2d_compact_args *a, const csa2p_cache *caches, int32_t n,
